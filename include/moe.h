@@ -377,6 +377,157 @@ int moe_forward_static(moe_shape s, const void* x, const void* Wg, const float* 
                        const void* W1, const void* W3, const void* W2, void* y,
                        int32_t* device_status, void* stream);
 
+/* ==========================================================================
+ * Scored routing and the int8 experts
+ *
+ * The second form of the layer: the router's logits are scored (softmax or
+ * sigmoid), steered by a selection bias and by groups of experts, and the experts'
+ * products run in 8-bit integers with a scale for each token row and each output
+ * channel.  Everything of the conventions above holds (device pointers, 16-byte
+ * alignment, dense row-major tensors, host checks before any launch, work on
+ * `stream`, nothing allocated, nothing synchronised).  Supported shapes
+ * (moe_check_shape_int8; moe_check_scoring for the routing alone): T >= 0,
+ * 1 <= k <= min(E, 16), E <= 512, d and d_ff multiples of 16 up to 131072 (the
+ * int32 sums are then exact), T*k <= 2^27.
+ * ======================================================================== */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_type;
+
+typedef struct {
+    int32_t score;       /* moe_score: s = softmax over the row's E logits, or their sigmoids */
+    int32_t n_group;     /* groups of E / n_group consecutive experts, 1 .. 32, dividing E */
+    int32_t topk_group;  /* groups kept, 1 .. n_group; k <= topk_group * E / n_group */
+    int32_t group_top;   /* a group's value: its largest choice (1), or the sum of its two largest (2) */
+    int32_t renorm;      /* nonzero: the gates of a token are divided by their sum */
+    float scale;         /* finite factor on every gate */
+} moe_scoring;
+
+/* Checks E, k and T of `s` (d and d_ff are ignored) and the scoring `r`. */
+int moe_check_scoring(moe_shape s, moe_scoring r);
+
+/*
+ * moe_route_scored -- experts and gates of each token from its router logits:
+ *     s_i = score of l_i,   c_i = s_i + bias_i,
+ *     the topk_group groups of largest value stay,
+ *     S = the k largest c_i left,   gate = scale * s_i [/ sum_{j in S} s_j]
+ *   logits [T,E] float or bf16 (logits_type) (in)
+ *   bias [E] float or NULL: steers the selection only, not the gates (in)
+ *   mask [T] uint8 or NULL: rows with 0 (padding) get no expert, whatever
+ *       their logits hold (in)
+ *   idx [T,k] int32: slot 0 = largest choice, ties -> lower id; -1 for a slot
+ *       that no expert fills (out)
+ *   gate [T,k] float; 0 where idx is -1 (out)
+ * Only s.T, s.E and s.k are used.  An expert whose logit (or choice) is -inf or
+ * NaN is never selected, so a row that has none left is all -1; +inf logits share
+ * the softmax among themselves.  Slots with idx -1 get no row from the dispatch
+ * and no term in the combine.  The selection is that of float64 scores: rows whose
+ * float32 choices lie too close to tell apart are decided in float64 (equal
+ * groups: the lower one).  Renormalised gates are formed relative to the largest
+ * selected score, so they do not underflow however negative the logits are.
+ */
+int moe_route_scored(moe_shape s, moe_scoring r, const void* logits, int logits_type,
+                     const float* bias, const uint8_t* mask, int32_t* idx, float* gate,
+                     void* stream);
+
+/*
+ * moe_route_scored_backward -- gradient of moe_route_scored's gates to the logits.
+ *   logits as above; idx [T,k] int32 from the forward call; dgate [T,k] float (in)
+ *   dlogits [T,E], the logits' type: every element is written (out)
+ * The selection is a constant, the bias has no gradient.  Slots whose idx lies
+ * outside 0..E-1, or names an expert whose logit is -inf or NaN, add nothing
+ * (their dgate is not looked at); an expert named by several slots gets their
+ * sum.  Only s.T, s.E, s.k, r.score, r.renorm and r.scale matter, but all of r is
+ * checked.
+ */
+int moe_route_scored_backward(moe_shape s, moe_scoring r, const void* logits, int logits_type,
+                              const int32_t* idx, const float* dgate, void* dlogits,
+                              void* stream);
+
+/* Checks a shape against the limits of the int8 layer without touching the GPU. */
+int moe_check_shape_int8(moe_shape s);
+
+/*
+ * moe_quantize_weights_int8 -- 8-bit weights, one scale for each output channel;
+ * run once when weights are loaded.
+ *   W [E,K,N] bf16 (the layout of W1, W3: K = d, N = d_ff; W2: K = d_ff, N = d) (in)
+ *   Wq [E,N,K] int8: Wq[e][n][k] = round(W[e][k][n] * 127 / amax), K fastest (out)
+ *   scale [E,N] float: amax / 127, amax = max_k |W[e][k][n]| (out)
+ * Rounding is to nearest, ties to even, of the exact quotient.  A channel of zeros has
+ * scale 0; one that holds an infinity or a NaN has scale NaN and zeros.
+ * 1 <= E <= 512, K and N multiples of 16 up to 131072.
+ */
+int moe_quantize_weights_int8(int E, int K, int N, const void* W, int8_t* Wq, float* scale,
+                              void* stream);
+
+/*
+ * moe_dispatch_int8 -- moe_dispatch whose sorted rows leave in 8 bits: each token
+ * row is read once, quantised (as a channel above; xs = its amax / 127) and written to its
+ * sorted rows.
+ *   idx, x as for moe_dispatch (in); offsets, perm_tok, inv as there (out)
+ *   xq [T*k,d] int8, xs [T*k] float (out)
+ * Rows at or beyond offsets[E] are left untouched.
+ */
+int moe_dispatch_int8(moe_shape s, const int32_t* idx, const void* x, int32_t* offsets,
+                      int32_t* perm_tok, int32_t* inv, int8_t* xq, float* xs, void* stream);
+
+/*
+ * moe_expert_swiglu_int8 -- the experts over their rows in 8-bit integers:
+ *     a = (xq W1q^T) xs s1,   b = (xq W3q^T) xs s3,   h = SiLU(a) (.) b  (bf16),
+ *     hq, hs = h's rows quantised,   o = (hq W2q^T) hs s2  (bf16)
+ *   xq [T*k,d] int8, xs [T*k] float, offsets [E+1] int32 (from moe_dispatch_int8) (in)
+ *   W1q, W3q [E,d_ff,d] int8 with s1, s3 [E,d_ff]; W2q [E,d,d_ff] int8 with s2 [E,d] (in)
+ *   o [T*k,d] bf16 (out)
+ *   ws: >= moe_expert_swiglu_int8_workspace_bytes(s) bytes of device memory
+ * The products are summed exactly in int32 and scaled in float32, row scale first;
+ * h is rounded to bf16 (the layer's own precision for it) before its rows are
+ * quantised, and o to bf16 (2^-9 against the 2^-8 and more of the 8-bit rows).
+ * Rows at or beyond offsets[E] are left untouched; an expert without rows costs
+ * nothing; a row's result does not depend on the other rows.  A row whose
+ * scale is NaN (x held an infinity or a NaN) gives NaN.  A device wait that
+ * expires leaves o incomplete and is reported by moe_read_device_status(ws).
+ */
+size_t moe_expert_swiglu_int8_workspace_bytes(moe_shape s);
+int moe_expert_swiglu_int8(moe_shape s, const int8_t* xq, const float* xs,
+                           const int32_t* offsets, const int8_t* W1q, const float* s1,
+                           const int8_t* W3q, const float* s3, const int8_t* W2q,
+                           const float* s2, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/* Test hook of the bounded waits: moe_expert_swiglu_int8 whose producers stop after
+ * `stall_after` (>= 0) pipeline stages, with every device wait bounded by
+ * `timeout_ns` (1e3 .. 2e9); see moe_expert_swiglu_stall_test. */
+int moe_expert_swiglu_int8_stall_test(moe_shape s, const int8_t* xq, const float* xs,
+                                      const int32_t* offsets, const int8_t* W1q,
+                                      const float* s1, const int8_t* W3q, const float* s3,
+                                      const int8_t* W2q, const float* s2, void* o, void* ws,
+                                      size_t ws_bytes, int stall_after, uint64_t timeout_ns,
+                                      void* stream);
+
+/*
+ * moe_combine_bf16 -- moe_combine over bf16 expert outputs:
+ * y[t] = sum over slots s (in slot order) of gate[t,s] * o[inv[t,s]], products and
+ * sums in float32 without fused multiply-add, y rounded once to bf16; slots with
+ * inv < 0 are skipped.
+ *   o [T*k,d] bf16, inv [T,k] int32, gate [T,k] float (in);  y [T,d] bf16 (out)
+ */
+int moe_combine_bf16(moe_shape s, const void* o, const int32_t* inv, const float* gate, void* y,
+                     void* stream);
+
+/*
+ * moe_forward_int8 -- the layer from tokens and router logits: moe_route_scored,
+ * moe_dispatch_int8, moe_expert_swiglu_int8, moe_combine_bf16, with their bits.
+ *   x [T,d] bf16, logits [T,E] float or bf16 (of moe_route, or of any router),
+ *   route_bias [E] float or NULL, mask [T] uint8 or NULL, weights as above (in)
+ *   y [T,d] bf16: 0 for a masked token (out)
+ *   idx_out [T,k] int32, gate_out [T,k] float: copies of the routing, or NULL
+ *   ws: >= moe_forward_int8_workspace_bytes(s) bytes of device memory
+ */
+size_t moe_forward_int8_workspace_bytes(moe_shape s);
+int moe_forward_int8(moe_shape s, const void* x, const void* logits, int logits_type,
+                     moe_scoring r, const float* route_bias, const uint8_t* mask,
+                     const int8_t* W1q, const float* s1, const int8_t* W3q, const float* s3,
+                     const int8_t* W2q, const float* s2, void* y, int32_t* idx_out,
+                     float* gate_out, void* ws, size_t ws_bytes, void* stream);
+
 /*
  * moe_read_device_status -- SYNCHRONISES `stream`, then reads the status word
  * that moe_expert_swiglu / moe_forward keep at the start of their workspace:

@@ -17,4 +17,8 @@ from .binding import (  # noqa: F401
     moe_forward_kernel_count, moe_forward_profiled, moe_forward_static,
     moe_forward_workspace_bytes,
     moe_read_device_status, moe_route, status_string, workspace,
+    MoeScoring, moe_check_scoring, moe_check_shape_int8, moe_combine_bf16, moe_dispatch_int8,
+    moe_expert_swiglu_int8, moe_expert_swiglu_int8_stall_test,
+    moe_expert_swiglu_int8_workspace_bytes, moe_forward_int8, moe_forward_int8_workspace_bytes,
+    moe_quantize_weights_int8, moe_route_scored, moe_route_scored_backward,
 )

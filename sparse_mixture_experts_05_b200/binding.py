@@ -35,6 +35,10 @@ EXPORTS = (
     "moe_forward_hostio_batches_stall_test",
     "moe_forward_static",
     "moe_aux_loss", "moe_block_workspace_bytes", "moe_block_forward", "moe_read_device_status",
+    "moe_check_scoring", "moe_route_scored", "moe_route_scored_backward", "moe_check_shape_int8",
+    "moe_quantize_weights_int8", "moe_dispatch_int8", "moe_expert_swiglu_int8_workspace_bytes",
+    "moe_expert_swiglu_int8", "moe_expert_swiglu_int8_stall_test", "moe_combine_bf16",
+    "moe_forward_int8_workspace_bytes", "moe_forward_int8",
 )
 
 MOE_STATIC_SCRATCH_BYTES = 8 << 20
@@ -43,6 +47,26 @@ MOE_STATIC_SCRATCH_BYTES = 8 << 20
 class MoeShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("d_ff", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32)]
+
+
+class MoeScoring(ctypes.Structure):
+    """Scores, groups and gates of moe_route_scored (moe_scoring of include/moe.h).
+
+    score: "softmax" over the row's logits or their "sigmoid"s; n_group groups of E / n_group
+    consecutive experts, of which the topk_group best stay, a group's value being
+    its largest choice (group_top = 1) or the sum of its two largest (2); renorm
+    divides a token's gates by their sum; scale multiplies them."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+    SCORES = {"softmax": 0, "sigmoid": 1}
+
+    def __init__(self, score="softmax", n_group=1, topk_group=1, group_top=1, renorm=True,
+                 scale=1.0):
+        if score not in self.SCORES:
+            raise ValueError(f"score must be one of {tuple(self.SCORES)}, got {score!r}")
+        super().__init__(self.SCORES[score], int(n_group), int(topk_group), int(group_top),
+                         int(bool(renorm)), float(scale))
 
 
 class MoeError(RuntimeError):
@@ -112,6 +136,30 @@ def lib() -> ctypes.CDLL:
         L.moe_block_forward.argtypes = [S, P, P, ctypes.c_float, P, P, P, P, P, P, P, Z, P]
         L.moe_aux_loss.restype = I
         L.moe_aux_loss.argtypes = [S, P, P, P, P, P, P, P]
+        C = MoeScoring
+        L.moe_check_scoring.restype = I
+        L.moe_check_scoring.argtypes = [S, C]
+        L.moe_check_shape_int8.restype = I
+        L.moe_check_shape_int8.argtypes = [S]
+        for fn in ("moe_expert_swiglu_int8_workspace_bytes", "moe_forward_int8_workspace_bytes"):
+            getattr(L, fn).restype = Z
+            getattr(L, fn).argtypes = [S]
+        L.moe_route_scored.restype = I
+        L.moe_route_scored.argtypes = [S, C, P, I, P, P, P, P, P]
+        L.moe_route_scored_backward.restype = I
+        L.moe_route_scored_backward.argtypes = [S, C, P, I, P, P, P, P]
+        L.moe_quantize_weights_int8.restype = I
+        L.moe_quantize_weights_int8.argtypes = [I, I, I, P, P, P, P]
+        L.moe_dispatch_int8.restype = I
+        L.moe_dispatch_int8.argtypes = [S, P, P, P, P, P, P, P, P]
+        L.moe_expert_swiglu_int8.restype = I
+        L.moe_expert_swiglu_int8.argtypes = [S] + [P] * 11 + [Z, P]
+        L.moe_expert_swiglu_int8_stall_test.restype = I
+        L.moe_expert_swiglu_int8_stall_test.argtypes = [S] + [P] * 11 + [Z, I, ctypes.c_uint64, P]
+        L.moe_combine_bf16.restype = I
+        L.moe_combine_bf16.argtypes = [S, P, P, P, P, P]
+        L.moe_forward_int8.restype = I
+        L.moe_forward_int8.argtypes = [S, P, P, I, C, P, P] + [P] * 6 + [P, P, P, P, Z, P]
         L.moe_read_device_status.restype = I
         L.moe_read_device_status.argtypes = [P, P]
         _lib = L
@@ -553,3 +601,195 @@ def moe_aux_loss(shape, logits, idx, mask=None, want_stats=False, stream=None):
 def moe_read_device_status(ws, stream=None) -> int:
     """Synchronises the stream and returns the status word of `ws` (MOE_OK or an error code)."""
     return lib().moe_read_device_status(_p(ws), _stream(stream))
+
+
+# ------------------------------------------------------------------ scored routing, int8 experts
+
+_LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _logits(t: torch.Tensor, shape) -> int:
+    T, d, d_ff, E, k = shape
+    if t.dtype not in _LOGITS_TYPES:
+        raise ValueError(f"logits must be float32 or bfloat16, got {t.dtype}")
+    _dev(t, "logits", t.dtype, (T, E))
+    return _LOGITS_TYPES[t.dtype]
+
+
+def moe_check_scoring(shape, scoring: MoeScoring) -> int:
+    return lib().moe_check_scoring(_shape(shape), scoring)
+
+
+def moe_check_shape_int8(shape) -> int:
+    return lib().moe_check_shape_int8(_shape(shape))
+
+
+def moe_expert_swiglu_int8_workspace_bytes(shape) -> int:
+    return lib().moe_expert_swiglu_int8_workspace_bytes(_shape(shape))
+
+
+def moe_forward_int8_workspace_bytes(shape) -> int:
+    return lib().moe_forward_int8_workspace_bytes(_shape(shape))
+
+
+def moe_route_scored(shape, logits, scoring: MoeScoring, bias=None, mask=None, idx=None, gate=None,
+                     stream=None):
+    """Experts and gates of each token from its router logits [T, E] (float32 or bfloat16).
+
+    `bias` [E] float32 steers the selection only; rows whose `mask` [T] uint8 is 0 get no expert.
+    Returns (idx [T, k] int32, gate [T, k] float32); idx -1 (gate 0) marks a slot that
+    no expert fills.  Only T, E and k of `shape` are used."""
+    T, d, d_ff, E, k = shape
+    kind = _logits(logits, shape)
+    _dev(bias, "bias", torch.float32, (E,))
+    _dev(mask, "mask", torch.uint8, (T,))
+    idx = _new((T, k), torch.int32, logits) if idx is None else idx
+    gate = _new((T, k), torch.float32, logits) if gate is None else gate
+    _dev(idx, "idx", torch.int32, (T, k))
+    _dev(gate, "gate", torch.float32, (T, k))
+    _check("moe_route_scored",
+           lib().moe_route_scored(_shape(shape), scoring, _p(logits), kind, _p(bias), _p(mask),
+                                  _p(idx), _p(gate), _stream(stream)))
+    return idx, gate
+
+
+def moe_route_scored_backward(shape, logits, scoring: MoeScoring, idx, dgate, dlogits=None,
+                              stream=None):
+    """Gradient of moe_route_scored's gates to the logits, in the logits' type.
+
+    `idx` is the forward call's; `dgate` [T, k] float32 the gates' gradient."""
+    T, d, d_ff, E, k = shape
+    kind = _logits(logits, shape)
+    _dev(idx, "idx", torch.int32, (T, k))
+    _dev(dgate, "dgate", torch.float32, (T, k))
+    dlogits = _new((T, E), logits.dtype, logits) if dlogits is None else dlogits
+    _dev(dlogits, "dlogits", logits.dtype, (T, E))
+    _check("moe_route_scored_backward",
+           lib().moe_route_scored_backward(_shape(shape), scoring, _p(logits), kind, _p(idx),
+                                           _p(dgate), _p(dlogits), _stream(stream)))
+    return dlogits
+
+
+def moe_quantize_weights_int8(W, Wq=None, scale=None, stream=None):
+    """(Wq [E, N, K] int8, scale [E, N] float32) of bf16 weights W [E, K, N]: one scale for
+    each output channel.  The pairs are what moe_expert_swiglu_int8 takes as W1, W3, W2."""
+    _dev(W, "W", torch.bfloat16)
+    if W.dim() != 3:
+        raise ValueError(f"W must have shape (E, K, N), got {tuple(W.shape)}")
+    E, K, N = W.shape
+    Wq = _new((E, N, K), torch.int8, W) if Wq is None else Wq
+    scale = _new((E, N), torch.float32, W) if scale is None else scale
+    _dev(Wq, "Wq", torch.int8, (E, N, K))
+    _dev(scale, "scale", torch.float32, (E, N))
+    _check("moe_quantize_weights_int8",
+           lib().moe_quantize_weights_int8(E, K, N, _p(W), _p(Wq), _p(scale), _stream(stream)))
+    return Wq, scale
+
+
+def moe_dispatch_int8(shape, idx, x, offsets=None, perm_tok=None, inv=None, xq=None, xs=None,
+                      stream=None):
+    """moe_dispatch whose sorted rows leave quantised: returns (offsets, perm_tok, inv,
+    xq [T*k, d] int8, xs [T*k] float32)."""
+    T, d, d_ff, E, k = shape
+    _dev(idx, "idx", torch.int32, (T, k))
+    _dev(x, "x", torch.bfloat16, (T, d))
+    offsets = _new((E + 1,), torch.int32, x) if offsets is None else offsets
+    perm_tok = _new((T * k,), torch.int32, x) if perm_tok is None else perm_tok
+    inv = _new((T, k), torch.int32, x) if inv is None else inv
+    xq = _new((T * k, d), torch.int8, x) if xq is None else xq
+    xs = _new((T * k,), torch.float32, x) if xs is None else xs
+    _dev(offsets, "offsets", torch.int32, (E + 1,))
+    _dev(perm_tok, "perm_tok", torch.int32, (T * k,))
+    _dev(inv, "inv", torch.int32, (T, k))
+    _dev(xq, "xq", torch.int8, (T * k, d))
+    _dev(xs, "xs", torch.float32, (T * k,))
+    _check("moe_dispatch_int8",
+           lib().moe_dispatch_int8(_shape(shape), _p(idx), _p(x), _p(offsets), _p(perm_tok),
+                                   _p(inv), _p(xq), _p(xs), _stream(stream)))
+    return offsets, perm_tok, inv, xq, xs
+
+
+def _int8_weights(shape, W1, W3, W2):
+    """Pointers of the (int8, scale) pairs W1, W3 [E, d_ff, d] and W2 [E, d, d_ff]."""
+    T, d, d_ff, E, k = shape
+    out = []
+    for name, pair, n, kk in (("W1", W1, d_ff, d), ("W3", W3, d_ff, d), ("W2", W2, d, d_ff)):
+        q, s = pair
+        _dev(q, name, torch.int8, (E, n, kk))
+        _dev(s, f"{name} scale", torch.float32, (E, n))
+        out += [_p(q), _p(s)]
+    return out
+
+
+def _int8_expert_args(shape, xq, xs, offsets, o, ws):
+    T, d, d_ff, E, k = shape
+    R = T * k
+    _dev(xq, "xq", torch.int8, (R, d))
+    _dev(xs, "xs", torch.float32, (R,))
+    _dev(offsets, "offsets", torch.int32, (E + 1,))
+    o = _new((R, d), torch.bfloat16, xq) if o is None else o
+    ws = workspace(moe_expert_swiglu_int8_workspace_bytes(shape), xq.device) if ws is None else ws
+    _dev(o, "o", torch.bfloat16, (R, d))
+    _dev(ws, "ws", torch.uint8)
+    return o, ws
+
+
+def moe_expert_swiglu_int8(shape, xq, xs, offsets, W1, W3, W2, o=None, ws=None, stream=None):
+    """The SwiGLU experts in 8-bit integers over the rows of moe_dispatch_int8.
+
+    W1, W3, W2 are the (int8, scale) pairs of moe_quantize_weights_int8.  Returns
+    (o [T*k, d] bfloat16, ws)."""
+    o, ws = _int8_expert_args(shape, xq, xs, offsets, o, ws)
+    weights = _int8_weights(shape, W1, W3, W2)
+    _check("moe_expert_swiglu_int8",
+           lib().moe_expert_swiglu_int8(_shape(shape), _p(xq), _p(xs), _p(offsets), *weights,
+                                        _p(o), _p(ws), ws.numel(), _stream(stream)))
+    return o, ws
+
+
+def moe_expert_swiglu_int8_stall_test(shape, xq, xs, offsets, W1, W3, W2, stall_after: int,
+                                      timeout_ns: int, o=None, ws=None, stream=None):
+    o, ws = _int8_expert_args(shape, xq, xs, offsets, o, ws)
+    weights = _int8_weights(shape, W1, W3, W2)
+    _check("moe_expert_swiglu_int8_stall_test",
+           lib().moe_expert_swiglu_int8_stall_test(_shape(shape), _p(xq), _p(xs), _p(offsets),
+                                                   *weights, _p(o), _p(ws), ws.numel(),
+                                                   int(stall_after), int(timeout_ns),
+                                                   _stream(stream)))
+    return o, ws
+
+
+def moe_combine_bf16(shape, o, inv, gate, y=None, stream=None):
+    T, d, d_ff, E, k = shape
+    _dev(o, "o", torch.bfloat16, (T * k, d))
+    _dev(inv, "inv", torch.int32, (T, k))
+    _dev(gate, "gate", torch.float32, (T, k))
+    y = _new((T, d), torch.bfloat16, o) if y is None else y
+    _dev(y, "y", torch.bfloat16, (T, d))
+    _check("moe_combine_bf16", lib().moe_combine_bf16(_shape(shape), _p(o), _p(inv), _p(gate),
+                                                      _p(y), _stream(stream)))
+    return y
+
+
+def moe_forward_int8(shape, x, logits, scoring: MoeScoring, W1, W3, W2, route_bias=None, mask=None,
+                     y=None, idx_out=None, gate_out=None, ws=None, stream=None):
+    """The layer with scored routing and int8 experts, from tokens x [T, d] bfloat16 and router
+    logits [T, E] (float32, as of moe_route, or bfloat16).  W1, W3, W2 are the
+    (int8, scale) pairs of moe_quantize_weights_int8."""
+    T, d, d_ff, E, k = shape
+    _dev(x, "x", torch.bfloat16, (T, d))
+    kind = _logits(logits, shape)
+    _dev(route_bias, "route_bias", torch.float32, (E,))
+    _dev(mask, "mask", torch.uint8, (T,))
+    weights = _int8_weights(shape, W1, W3, W2)
+    y = _new((T, d), torch.bfloat16, x) if y is None else y
+    ws = workspace(moe_forward_int8_workspace_bytes(shape), x.device) if ws is None else ws
+    _dev(y, "y", torch.bfloat16, (T, d))
+    _dev(idx_out, "idx_out", torch.int32, (T, k))
+    _dev(gate_out, "gate_out", torch.float32, (T, k))
+    _dev(ws, "ws", torch.uint8)
+    _check("moe_forward_int8",
+           lib().moe_forward_int8(_shape(shape), _p(x), _p(logits), kind, scoring, _p(route_bias),
+                                  _p(mask), *weights, _p(y), _p(idx_out), _p(gate_out), _p(ws),
+                                  ws.numel(), _stream(stream)))
+    return y

@@ -1,0 +1,488 @@
+// int8_rows.cu -- row kernels of the int8 layer: token lists for up to 512 experts,
+// rows and weight channels quantised to 8 bits, combine of bf16 expert outputs.
+//
+// Quantisation of a vector v of bf16 values (a token row, or an output channel):
+//     amax = max |v_i|,   q_i = rint(v_i * 127 / amax),   scale = amax / 127
+// q_i is the exact quotient rounded to nearest, ties to even.  One multiplication
+// by r = 127 / amax rounded up gives it: v_i and amax have 8-bit significands, so
+// a quotient that is no tie is at least 1 / (254 * 255) of its size away from one
+// (127 v_i 2 and (2n + 1) amax are integers of at most 16 bits, scaled alike),
+// against the 2^-23 by which r exceeds 127 / amax; and the only tie is
+// |v_i| = amax / 2 (127 is prime, so it has to divide 2n + 1 < 255), where the
+// quotient 63.5, exact or rounded up, goes to the even 64 either way.  The product and the
+// rounding are one fused multiply-add onto 1.5 * 2^23, whose low byte is q_i.
+// Where 127 / amax would leave the float range (amax below 1e-30) both sides are
+// scaled by 2^100 first.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "dispatch.cuh"
+#include "int8_rows.cuh"
+#include "sm100.cuh"
+
+namespace moe {
+namespace int8rows {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// ------------------------------------------------------------------ quantisation
+// Multiplier of a vector whose largest |value| has the bf16 bits `amax`, and its scale.
+struct Quant {
+    float pre, r, scale;
+};
+
+__device__ __forceinline__ Quant make_quant(uint32_t amax) {
+    Quant q;
+    q.pre = 1.0f;
+    if (amax >= 0x7f80u) {  // an infinity or a NaN: zeros, and a scale that shows it
+        q.r = 0.0f;
+        q.scale = __uint_as_float(0x7fc00000u);
+        return q;
+    }
+    const float a = __uint_as_float(amax << 16);
+    q.scale = __fdiv_rn(a, 127.0f);
+    if (a < 1e-30f) q.pre = 0x1p100f;
+    q.r = a > 0.0f ? __fdiv_ru(127.0f, a * q.pre) : 0.0f;
+    return q;
+}
+
+// Two bf16 values: the low 16 bits hold q of the low one, the high 16 q of the high
+// one, each in its low byte.
+__device__ __forceinline__ uint32_t quantize2(uint32_t v, const Quant& q) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+    const float lo = __fmaf_rn(bf16_lo(v) * q.pre, q.r, kMagic);
+    const float hi = __fmaf_rn(bf16_hi(v) * q.pre, q.r, kMagic);
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+}
+
+// Four bf16 values in two words to four bytes.  (An infinity times 0 is NaN: the
+// caller zeroes rows that hold one.)
+__device__ __forceinline__ uint32_t quantize4(uint32_t v0, uint32_t v1, const Quant& q) {
+    return __byte_perm(quantize2(v0, q), quantize2(v1, q), 0x6420);
+}
+
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t v) {
+    return __vmaxu2(m, v & 0x7fff7fffu);
+}
+
+// 16 bf16 values (two uint4) to 16 bytes.
+__device__ __forceinline__ uint4 quantize16(const uint4& a, const uint4& b, const Quant& q) {
+    if (q.r == 0.0f) return make_uint4(0u, 0u, 0u, 0u);
+    return make_uint4(quantize4(a.x, a.y, q), quantize4(a.z, a.w, q), quantize4(b.x, b.y, q),
+                      quantize4(b.z, b.w, q));
+}
+
+__device__ __forceinline__ uint32_t max_abs16(const uint4& a, const uint4& b, uint32_t m) {
+    m = max_abs2(max_abs2(max_abs2(max_abs2(m, a.x), a.y), a.z), a.w);
+    return max_abs2(max_abs2(max_abs2(max_abs2(m, b.x), b.y), b.z), b.w);
+}
+
+// Largest of both halves over the block (every thread returns it).
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* s_max) {
+    uint32_t one = max(m & 0xffffu, m >> 16);
+    one = __reduce_max_sync(kAll, one);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return one;
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = one;
+    __syncthreads();
+    uint32_t all = 0;
+    for (int w = 0; w < warps; ++w) all = max(all, s_max[w]);
+    return all;
+}
+
+// One block quantises one row of `units` x 16 values; NU > 0: the row stays in
+// registers (NU units a thread), 0: it is read twice (the second time from L2).
+// kScatter: row t = blockIdx.x goes to its k sorted rows; otherwise to row t
+// itself, if t < *n_rows.
+template <int NU, bool kScatter>
+__global__ void __launch_bounds__(256)
+    quantize_kernel(const uint4* __restrict__ x, int units, const int32_t* __restrict__ map, int k,
+                    uint4* __restrict__ xq, float* __restrict__ xs, uint32_t* zero,
+                    int64_t zero_words) {
+    __shared__ uint32_t s_max[8];
+    grid_dependency_wait();
+    const int64_t row = blockIdx.x;
+    if (kScatter) {
+        for (int64_t i = row * blockDim.x + threadIdx.x; i < zero_words;
+             i += (int64_t)gridDim.x * blockDim.x)
+            zero[i] = 0u;
+    } else if (row >= __ldg(map)) {
+        return;
+    }
+    const uint4* src = x + row * units * 2;
+    uint4 v[NU > 0 ? NU : 1][2];
+    uint32_t m = 0;
+    if constexpr (NU > 0) {
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            const int u = threadIdx.x + n * blockDim.x;
+            v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (u < units) {
+                v[n][0] = __ldg(src + 2 * u);
+                v[n][1] = __ldg(src + 2 * u + 1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NU; ++n) m = max_abs16(v[n][0], v[n][1], m);
+    } else {
+        for (int u = threadIdx.x; u < units; u += blockDim.x)
+            m = max_abs16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), m);
+    }
+    const Quant q = make_quant(block_max(m, s_max));
+    const int copies = kScatter ? k : 1;
+    for (int s = 0; s < copies; ++s) {
+        const int64_t dst = kScatter ? (int64_t)__ldg(map + row * k + s) : row;
+        if (dst < 0) continue;
+        if (threadIdx.x == 0) xs[dst] = q.scale;
+        if constexpr (NU > 0) {
+#pragma unroll
+            for (int n = 0; n < NU; ++n) {
+                const int u = threadIdx.x + n * blockDim.x;
+                if (u < units) xq[dst * units + u] = quantize16(v[n][0], v[n][1], q);
+            }
+        } else {
+            for (int u = threadIdx.x; u < units; u += blockDim.x)
+                xq[dst * units + u] = quantize16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), q);
+        }
+    }
+}
+
+template <bool kScatter>
+int launch_quantize(const void* x, int64_t rows, int cols, const int32_t* map, int k, int8_t* xq,
+                    float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t st) {
+    const int units = cols / 16;
+    const int threads = std::min(256, (units + 31) / 32 * 32);
+    const int per = (units + threads - 1) / threads;
+    auto kern = per <= 1   ? quantize_kernel<1, kScatter>
+                : per <= 2 ? quantize_kernel<2, kScatter>
+                : per <= 4 ? quantize_kernel<4, kScatter>
+                           : quantize_kernel<0, kScatter>;
+    return launch_pdl(kern, dim3((unsigned)rows), dim3(threads), 0, st,
+                      static_cast<const uint4*>(x), units, map, k, reinterpret_cast<uint4*>(xq),
+                      xs, zero, zero_words) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ weights
+// W [E][K][N] bf16 -> Wq [E][N][K] int8.  One block takes 64 channels of one
+// expert: a pass over their K rows for the channels' amax (whole 128-byte rows of W),
+// then a second pass that quantises 128 rows at a time and turns them through
+// shared memory, so that Wq is written in 128-byte runs.  Run once at load time.
+constexpr int kWCols = 64;
+constexpr int kWRows = 128;
+
+__global__ void __launch_bounds__(256)
+    weights_kernel(const uint4* __restrict__ W, int K, int N, int8_t* __restrict__ Wq,
+                   float* __restrict__ scale) {
+    __shared__ uint32_t s_amax[kWCols];
+    __shared__ Quant s_q[kWCols];
+    __shared__ __align__(16) uint8_t s_tile[kWCols][kWRows + 16];
+    grid_dependency_wait();
+    const int blocks_n = (N + kWCols - 1) / kWCols;
+    const int e = blockIdx.x / blocks_n;
+    const int n0 = (blockIdx.x - e * blocks_n) * kWCols;
+    const int chunk = threadIdx.x & 7;   // 8 columns each
+    const int r0 = threadIdx.x >> 3;     // 32 rows a step
+    const bool in = n0 + chunk * 8 < N;  // N is a multiple of 8
+    const uint4* src = W + ((int64_t)e * K * N + n0) / 8 + chunk;
+    const int64_t pitch = N / 8;
+    if (threadIdx.x < kWCols) s_amax[threadIdx.x] = 0u;
+    uint32_t m[4] = {0u, 0u, 0u, 0u};
+    if (in) {
+#pragma unroll 4
+        for (int k = r0; k < K; k += 32) {
+            const uint4 v = __ldg(src + k * pitch);
+            m[0] = max_abs2(m[0], v.x);
+            m[1] = max_abs2(m[1], v.y);
+            m[2] = max_abs2(m[2], v.z);
+            m[3] = max_abs2(m[3], v.w);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        atomicMax(&s_amax[chunk * 8 + 2 * j], m[j] & 0xffffu);
+        atomicMax(&s_amax[chunk * 8 + 2 * j + 1], m[j] >> 16);
+    }
+    __syncthreads();
+    if (threadIdx.x < kWCols) {
+        const Quant q = make_quant(s_amax[threadIdx.x]);
+        s_q[threadIdx.x] = q;
+        if (n0 + (int)threadIdx.x < N) scale[(int64_t)e * N + n0 + threadIdx.x] = q.scale;
+    }
+    __syncthreads();
+    Quant q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = s_q[chunk * 8 + j];
+    for (int k0 = 0; k0 < K; k0 += kWRows) {
+#pragma unroll
+        for (int s = 0; s < kWRows / 32; ++s) {
+            const int k = k0 + s * 32 + r0;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (in && k < K) v = __ldg(src + k * pitch);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t one = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+                s_tile[chunk * 8 + j][s * 32 + r0] =
+                    q[j].r == 0.0f ? (uint8_t)0 : (uint8_t)quantize2(one, q[j]);
+            }
+        }
+        __syncthreads();
+        // 64 channels x 128 bytes: 8 threads of 16 bytes a channel, two channels a thread
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int c = s * 32 + r0;
+            const int k = k0 + chunk * 16;
+            if (n0 + c < N && k < K)
+                *reinterpret_cast<uint4*>(Wq + ((int64_t)e * N + n0 + c) * K + k) =
+                    *reinterpret_cast<const uint4*>(&s_tile[c][chunk * 16]);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ token lists
+// The index kernel of the dispatch for more experts: the same cluster of C CTAs and the
+// same contiguous runs of slots per warp, with a counter for each (warp, expert) in
+// shared memory.  Thread e scans expert e's counters over the CTA's 32 warps and
+// reads the other CTAs' totals through distributed shared memory; a scan over
+// the experts gives their first rows.  Stable, deterministic, no atomics on positions.
+constexpr int kIndexThreads = 1024;
+constexpr int kIndexWarps = 32;
+constexpr int kMaxE = 512;
+constexpr int kMaxCluster = 8;
+constexpr int kSlotsPerWarp = 64;
+constexpr int kBatch = 8;
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__global__ void __launch_bounds__(kIndexThreads, 1)
+    index_many_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int k,
+                      int32_t* __restrict__ offsets, int32_t* __restrict__ perm_tok,
+                      int32_t* __restrict__ inv) {
+    extern __shared__ int s_pos[];  // [32][E]: counts, then next positions
+    __shared__ int s_total[kMaxE];
+    __shared__ int s_warp[kIndexWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)sm100::cluster_ctarank();
+    const int C = (int)cluster_ctas();
+    int* pos = s_pos + warp * E;
+    for (int e = lane; e < E; e += 32) pos[e] = 0;
+    __syncwarp();
+    grid_dependency_wait();
+    const int64_t per_warp = ((n + kIndexWarps * C - 1) / (kIndexWarps * C) + 31) / 32 * 32;
+    const int64_t j0 = min(n, (int64_t)(rank * kIndexWarps + warp) * per_warp);
+    const int64_t j1 = min(n, j0 + per_warp);
+    const unsigned lt = (1u << lane) - 1u;
+    for (int64_t base = j0; base < j1; base += 32 * kBatch) {
+        int ids[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t j = base + u * 32 + lane;
+            ids[u] = j < j1 ? __ldg(idx + j) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (base + u * 32 >= j1) break;
+            const bool valid = ids[u] >= 0 && ids[u] < E;
+            const unsigned same = __match_any_sync(kAll, valid ? ids[u] : -1);
+            if (valid && (same & lt) == 0) pos[ids[u]] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    int mine = 0;  // rows of expert `tid` in this CTA
+    if (tid < E) {
+        for (int w = 0; w < kIndexWarps; ++w) {
+            const int c = s_pos[w * E + tid];
+            s_pos[w * E + tid] = mine;
+            mine += c;
+        }
+        s_total[tid] = mine;
+    }
+    sm100::cluster_sync_all();
+    int before = 0, total = 0;
+    if (tid < E) {
+        const uint32_t at = sm100::smem_u32(&s_total[tid]);
+        for (int c = 0; c < C; ++c) {
+            const int t = ld_cluster_s32(sm100::map_to_cta(at, (uint32_t)c));
+            if (c < rank) before += t;
+            total += t;
+        }
+    }
+    int incl = total;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int start = incl - total;
+    for (int w = 0; w < warp; ++w) start += s_warp[w];
+    if (rank == 0) {
+        if (tid < E) offsets[tid] = start;
+        if (tid == E - 1) offsets[E] = start + total;
+    }
+    if (tid < E) {
+        for (int w = 0; w < kIndexWarps; ++w) s_pos[w * E + tid] += start + before;
+    }
+    __syncthreads();
+    for (int64_t base = j0; base < j1; base += 32 * kBatch) {
+        int ids[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t j = base + u * 32 + lane;
+            ids[u] = j < j1 ? __ldg(idx + j) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (base + u * 32 >= j1) break;
+            const int64_t j = base + u * 32 + lane;
+            const bool valid = ids[u] >= 0 && ids[u] < E;
+            const unsigned same = __match_any_sync(kAll, valid ? ids[u] : -1);
+            if (valid) {
+                const int p = pos[ids[u]] + __popc(same & lt);
+                perm_tok[p] = (int)(j / k);
+                inv[j] = p;
+            } else if (j < j1) {
+                inv[j] = -1;
+            }
+            __syncwarp();
+            if (valid && (same & lt) == 0) pos[ids[u]] += __popc(same);
+            __syncwarp();
+        }
+    }
+    sm100::cluster_sync_all();  // nobody leaves while its totals may still be read
+}
+
+// ------------------------------------------------------------------ combine
+// One thread per (token, 8 columns); the k rows' loads are issued before any is used.
+template <int KMAX>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const uint4* __restrict__ o, const int32_t* __restrict__ inv,
+                   const float* __restrict__ gate, int T, int d8, int k, uint4* __restrict__ y) {
+    grid_dependency_wait();
+    const int64_t total = (int64_t)T * d8;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
+        const int64_t t = i / d8;
+        const int c = (int)(i - t * d8);
+        uint4 v[KMAX];
+        float g[KMAX];
+        bool has[KMAX];
+#pragma unroll
+        for (int s = 0; s < KMAX; ++s) {
+            const int row = s < k ? __ldg(inv + t * k + s) : -1;
+            has[s] = row >= 0;
+            if (has[s]) {
+                g[s] = __ldg(gate + t * k + s);
+                v[s] = __ldg(o + (int64_t)row * d8 + c);
+            }
+        }
+        float acc[8];
+        bool first = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KMAX; ++s) {
+            if (!has[s]) continue;
+            const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = __fmul_rn(g[s], (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]));
+                acc[j] = first ? p : __fadd_rn(acc[j], p);
+            }
+            first = false;
+        }
+        y[i] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                          pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+    }
+}
+
+}  // namespace int8rows
+
+int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* offsets,
+                               int32_t* perm_tok, int32_t* inv, cudaStream_t stream) {
+    using namespace int8rows;
+    if (s.E <= 32) return launch_dispatch_index(s, idx, offsets, perm_tok, inv, stream);
+    const int64_t n = (int64_t)s.T * s.k;
+    int C = 1;
+    while (C < kMaxCluster && n > (int64_t)C * kIndexWarps * kSlotsPerWarp) C *= 2;
+    const int smem = kIndexWarps * s.E * 4;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(index_many_kernel),
+                             kIndexWarps * kMaxE * 4))
+        return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kIndexThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, n, (int)s.E, (int)s.k, offsets,
+                              perm_tok, inv) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+int launch_quantize_scatter(const moe_shape& s, const void* x, const int32_t* inv, int8_t* xq,
+                            float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t stream) {
+    return int8rows::launch_quantize<true>(x, s.T, s.d, inv, s.k, xq, xs, zero, zero_words, stream);
+}
+
+int launch_quantize_rows(const void* h, int max_rows, int cols, const int32_t* n_rows, int8_t* hq,
+                         float* hs, cudaStream_t stream) {
+    return int8rows::launch_quantize<false>(h, max_rows, cols, n_rows, 1, hq, hs, nullptr, 0,
+                                            stream);
+}
+
+int launch_quantize_weights(int E, int K, int N, const void* W, int8_t* Wq, float* scale,
+                            cudaStream_t stream) {
+    using namespace int8rows;
+    const int64_t blocks = (int64_t)E * ((N + kWCols - 1) / kWCols);
+    return launch_pdl(weights_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
+                      static_cast<const uint4*>(W), K, N, Wq, scale) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+int launch_combine_bf16(const moe_shape& s, const void* o, const int32_t* inv, const float* gate,
+                        void* y, cudaStream_t stream) {
+    using namespace int8rows;
+    const int64_t work = (int64_t)s.T * (s.d / 8);
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((work + 255) / 256,
+                                                                 (int64_t)device_sm_count() * 8));
+    auto kern = s.k <= 2   ? combine_kernel<2>
+                : s.k <= 4 ? combine_kernel<4>
+                : s.k <= 8 ? combine_kernel<8>
+                           : combine_kernel<16>;
+    return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(o), inv,
+                      gate, s.T, s.d / 8, s.k, static_cast<uint4*>(y)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+}  // namespace moe

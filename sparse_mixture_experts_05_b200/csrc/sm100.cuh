@@ -79,6 +79,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
 }
 
+// Per-stage wait: when the phase completes within try_wait's own suspend window
+// the abort flag is not read; otherwise a bounded wait, then the flag.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                           volatile int& abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, timeout_ns) && !abort_flag;
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -278,6 +286,28 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem], signed 8-bit inputs, int32 accumulation; issued
+// by one thread (pair: of the leader CTA, over both CTAs' shared and tensor memory).
+__device__ __forceinline__ void tc_mma_s8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_s8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrives once on the mbarrier at `bar_cluster_addr` (either CTA of the pair)
 // when every pair MMA issued so far by this thread has completed.
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar_cluster_addr) {
@@ -334,6 +364,15 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
            | ((b_mn_major ? 1u : 0u) << 16)       // B major
            | ((uint32_t)(N >> 3) << 17)           // N / 8
            | ((uint32_t)(M >> 4) << 24);          // M / 16
+}
+
+// Instruction descriptor for kind::i8 with signed A/B, both K-major, and int32 D.
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
+    return (2u << 4)                      // D format: S32
+           | (1u << 7)                    // A format: signed 8-bit
+           | (1u << 10)                   // B format: signed 8-bit
+           | ((uint32_t)(N >> 3) << 17)   // N / 8
+           | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
 }  // namespace sm100

@@ -1,0 +1,288 @@
+"""Scored routing and its gradient against float64 references: score kinds, biases,
+groups, top-k, renormalisation, logits that are infinite, NaN or masked, ties
+closer than float32 resolves, strides past 32 bits, streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_05_b200 as moe
+
+import _scored as ref
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def _logits(T, E, seed, dtype=torch.float32):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    return (2.0 * torch.randn(T, E, generator=gen, device="cuda")).to(dtype)
+
+
+def _run(l, k, sc, bias=None, mask=None):
+    T, E = l.shape
+    return moe.moe_route_scored((T, 128, 128, E, k), l, moe.MoeScoring(**sc), bias=bias, mask=mask)
+
+
+def _check(l, k, sc, bias=None, mask=None):
+    idx, gate = _run(l, k, sc, bias, mask)
+    r_idx, r_gate = ref.route(l, k, sc, bias, mask)
+    assert np.array_equal(idx.cpu().numpy(), r_idx)
+    g = gate.double().cpu().numpy()
+    ln = l.double().cpu().numpy()
+    fin = np.where(np.isfinite(ln), ln, 0.0)
+    spread = (fin.max(1) - fin.min(1))[:, None]
+    # gates below float32's smallest normal number are off by its spacing
+    bound = np.abs(r_gate) * ref.gate_rel(spread, l.shape[1]) + 2.0 ** -140
+    assert np.all(np.abs(g - r_gate) <= bound), float(np.max(np.abs(g - r_gate) / bound))
+    return idx, gate
+
+
+CASES = [
+    # E, k, scoring
+    (1, 1, dict(score="softmax")),
+    (2, 2, dict(score="sigmoid", renorm=False)),
+    (8, 2, dict(score="softmax")),
+    (8, 2, dict(score="softmax", renorm=False, scale=0.5)),
+    (16, 16, dict(score="sigmoid")),
+    (31, 5, dict(score="softmax", renorm=False)),
+    (32, 4, dict(score="softmax", n_group=8, topk_group=3)),
+    (33, 7, dict(score="sigmoid", n_group=3, topk_group=2, group_top=2)),
+    (60, 4, dict(score="softmax", n_group=6, topk_group=2, group_top=2)),
+    (64, 6, dict(score="softmax", n_group=8, topk_group=3, group_top=1, scale=16.0)),
+    (100, 9, dict(score="sigmoid", n_group=10, topk_group=4, group_top=2)),
+    (128, 8, dict(score="sigmoid", n_group=32, topk_group=4, group_top=2)),
+    (160, 6, dict(score="softmax", n_group=8, topk_group=3, renorm=False)),
+    (256, 8, dict(score="sigmoid", n_group=8, topk_group=4, group_top=2, scale=2.5)),
+    (257, 3, dict(score="sigmoid")),
+    (300, 10, dict(score="softmax", n_group=5, topk_group=5, group_top=2)),
+    (512, 16, dict(score="sigmoid", n_group=16, topk_group=2, group_top=2)),
+    (512, 8, dict(score="softmax", renorm=False)),
+]
+
+
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_routing_against_float64(case, dtype, biased):
+    E, k, sc = CASES[case]
+    for T in (1, 67):
+        l = _logits(T, E, 100 + case, dtype)
+        bias = None
+        if biased:
+            gen = torch.Generator("cuda").manual_seed(case)
+            bias = 0.3 * torch.randn(E, generator=gen, device="cuda")
+        _check(l, k, sc, bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+def test_infinite_nan_and_lowest_logits(score, renorm, grouped, biased):
+    E, k = 24, 5
+    l = _logits(12, E, 7)
+    lowest = torch.finfo(torch.float32).min
+    l[0] = -INF                       # nothing is left
+    l[1, 3:] = -INF                   # fewer experts than slots
+    l[2] = lowest                     # all at the type's lowest value
+    l[3, ::2] = lowest
+    l[4] = float("nan")
+    l[5, 1::2] = float("nan")
+    l[6, :3] = INF                    # several infinities share the softmax
+    l[7] = -300.0 - torch.arange(E, device="cuda")  # sigmoids below float32's range
+    l[8] = 200.0
+    l[9, :12] = -INF                  # whole groups gone
+    l[10, 5] = INF
+    l[11] = 0.0
+    l[11, 4] = -0.0                   # the two zeros tie
+    sc = dict(score=score, renorm=renorm, scale=1.5)
+    if grouped:
+        sc.update(n_group=4, topk_group=2, group_top=2)
+    bias = None
+    if biased:
+        bias = torch.linspace(-0.2, 0.3, E, device="cuda")
+        bias[20] = -INF               # an expert taken out by its bias
+    idx, gate = _check(l, k, sc, bias)
+    assert torch.all(idx[0] == -1) and torch.all(gate[0] == 0)
+    assert torch.all(idx[4] == -1)
+    if renorm and not biased:
+        assert abs(float(gate[7].sum()) - 1.5) < 1e-5
+
+
+def test_masked_rows_get_no_expert_whatever_they_hold():
+    l = _logits(40, 64, 3)
+    mask = torch.ones(40, dtype=torch.uint8, device="cuda")
+    mask[30:] = 0
+    mask[4] = 0
+    l[30:] = float("nan")
+    l[4] = INF
+    idx, gate = _check(l, 6, dict(score="softmax", renorm=False), mask=mask)
+    assert torch.all(idx[30:] == -1) and torch.all(gate[30:] == 0) and torch.all(idx[4] == -1)
+    mask.zero_()
+    idx, gate = _check(l, 6, dict(score="sigmoid"), mask=mask)
+    assert torch.all(idx == -1) and torch.all(gate == 0)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 1), (256, 8)])
+def test_choices_closer_than_float32_resolves(E, groups):
+    """Sigmoids of 18 .. 34 are all 1 in float32 but distinct in float64; biased
+    choices that differ by 1e-9 likewise."""
+    T = 50
+    gen = torch.Generator("cuda").manual_seed(5)
+    steps = torch.linspace(18.0, 34.0, E, device="cuda")
+    l = torch.stack([steps[torch.randperm(E, generator=gen, device="cuda")] for _ in range(T)])
+    sc = dict(score="sigmoid", n_group=groups, topk_group=max(1, groups // 2), group_top=2)
+    _check(l, 8, sc, torch.zeros(E, device="cuda"))
+    _check(l, 8, sc)
+    # s + b nearly equal for all experts: b = 1 - s rounded to float32
+    l = _logits(T, E, 6)
+    l[:] = l[0]
+    bias = (1.0 - torch.sigmoid(l[0].double())).float()
+    _check(l, 8, sc, bias)
+    sc["score"] = "softmax"
+    bias = (1.0 - torch.softmax(l[0].double(), 0)).float()
+    _check(l, 8, sc, bias)
+
+
+def test_equal_choices_go_to_the_lower_index():
+    l = torch.zeros(3, 256, device="cuda")
+    l[1, 100:] = 1.0
+    l[2, ::7] = 2.0
+    for sc in (dict(score="softmax"), dict(score="sigmoid", n_group=8, topk_group=4, group_top=2)):
+        idx, _ = _check(l, 8, sc)
+        assert idx[0].tolist() == list(range(8))
+        _check(l, 8, sc, torch.full((256,), 0.25, device="cuda"))
+
+
+def test_rows_past_32_bit_offsets():
+    E, k = 512, 4
+    T = (1 << 31) // E + 77
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    l[-80:] = _logits(80, E, 9, torch.bfloat16)
+    sc = dict(score="softmax", renorm=False)
+    idx, gate = _run(l, k, sc)
+    r_idx, r_gate = ref.route(l[-80:], k, sc)
+    assert np.array_equal(idx[-80:].cpu().numpy(), r_idx)
+    assert np.allclose(gate[-80:].cpu().numpy(), r_gate, rtol=1e-5)
+    dgate = torch.ones(T, k, device="cuda")
+    grad = moe.moe_route_scored_backward((T, 128, 128, E, k), l, moe.MoeScoring(**sc), idx, dgate)
+    r_grad, bound = ref.route_backward(l[-80:], idx[-80:], dgate[-80:], sc)
+    g = grad[-80:].double().cpu().numpy()
+    assert np.all(np.abs(g - r_grad) <= bound + np.abs(r_grad) * 2.0 ** -8 + 1e-38)
+
+
+# ------------------------------------------------------------------ gradient
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_gradient_against_float64(case, dtype):
+    E, k, sc = CASES[case]
+    for T in (1, 67):
+        l = _logits(T, E, 300 + case, dtype)
+        idx, _ = _run(l, k, sc)
+        gen = torch.Generator("cuda").manual_seed(case)
+        dgate = torch.randn(T, k, generator=gen, device="cuda")
+        if T > 1:
+            idx[5] = -1                     # a masked row
+            idx[6, 0] = -1                  # an unfilled slot
+            dgate[5] = float("nan")         # ... whose gradient is not looked at
+            dgate[6, 0] = INF
+            l[5] = float("nan")
+            if k > 1:
+                idx[7, 1] = idx[7, 0]       # the same expert twice
+            idx[8, 0] = E                   # outside the experts
+        got = torch.full((T, E), 7.0, dtype=dtype, device="cuda")
+        moe.moe_route_scored_backward((T, 128, 128, E, k), l, moe.MoeScoring(**sc), idx, dgate,
+                                      dlogits=got)
+        want, bound = ref.route_backward(l, idx, dgate, sc)
+        g = got.double().cpu().numpy()
+        step = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+        bound = bound + np.abs(want) * step + 2.0 ** -133
+        assert np.all(np.abs(g - want) <= bound), float(np.max(np.abs(g - want) / bound))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_against_differences(score, renorm):
+    """Central differences of the float64 gates, step 1e-6: truncation below
+    1e-11, rounding below 1e-9, against float32's bound of about 1e-6."""
+    E, k, T = 20, 4, 6
+    sc = dict(score=score, renorm=renorm, scale=2.0)
+    l = _logits(T, E, 11)
+    idx, _ = _run(l, k, sc)
+    dgate = torch.randn(T, k, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    got = moe.moe_route_scored_backward((T, 128, 128, E, k), l, moe.MoeScoring(**sc), idx, dgate)
+    ln, ix, dg = l.double().cpu().numpy(), idx.cpu().numpy(), dgate.double().cpu().numpy()
+
+    def loss(row, t):
+        return 2.0 * float((ref._weights(row, ix[t], score, renorm) * dg[t]).sum())
+    want = np.zeros((T, E))
+    for t in range(T):
+        for i in range(E):
+            up, down = ln[t].copy(), ln[t].copy()
+            up[i] += 1e-6
+            down[i] -= 1e-6
+            want[t, i] = (loss(up, t) - loss(down, t)) / 2e-6
+    assert np.all(np.abs(got.cpu().numpy() - want) <= 1e-5)
+
+
+def test_infinite_logits_in_the_gradient():
+    l = _logits(4, 16, 2)
+    l[0, 3:] = -INF
+    l[1, 2] = INF
+    l[2, ::2] = float("nan")
+    for sc in (dict(score="softmax", renorm=False), dict(score="softmax"),
+               dict(score="sigmoid"), dict(score="sigmoid", renorm=False)):
+        idx, _ = _run(l, 4, sc)
+        dgate = torch.ones(4, 4, device="cuda")
+        dgate[:, 1] = -2.0
+        got = moe.moe_route_scored_backward((4, 128, 128, 16, 4), l, moe.MoeScoring(**sc), idx, dgate)
+        want, bound = ref.route_backward(l, idx, dgate, sc)
+        assert np.all(np.abs(got.double().cpu().numpy() - want) <= bound + 1e-37)
+
+
+# ------------------------------------------------------------------ streams, graphs, layer
+
+def test_graph_replay_and_other_streams():
+    T, E, k = 300, 256, 8
+    sc = moe.MoeScoring(score="sigmoid", n_group=8, topk_group=4, group_top=2, scale=2.5)
+    shape = (T, 128, 128, E, k)
+    bias = 0.1 * torch.randn(E, device="cuda")
+    static, dgate = _logits(T, E, 1), torch.randn(T, k, device="cuda")
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    gate = torch.empty(T, k, device="cuda")
+    grad = torch.empty(T, E, device="cuda")
+
+    def step(l, i, g, dl):
+        moe.moe_route_scored(shape, l, sc, bias=bias, idx=i, gate=g)
+        moe.moe_route_scored_backward(shape, l, sc, i, dgate, dlogits=dl)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(static, idx, gate, grad)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(static, idx, gate, grad)
+    for seed in (2, 3):
+        l = _logits(T, E, seed)
+        static.copy_(l)
+        graph.replay()
+        e_idx, e_gate = moe.moe_route_scored(shape, l, sc, bias=bias)
+        e_grad = moe.moe_route_scored_backward(shape, l, sc, e_idx, dgate)
+        torch.cuda.synchronize()
+        assert torch.equal(idx, e_idx) and torch.equal(gate, e_gate) and torch.equal(grad, e_grad)
+
+
+def test_equals_the_layers_router_on_its_logits():
+    """Softmax over the selected two: the same experts, gates within both kernels'
+    float32 error (1e-6), as moe_route gives."""
+    T, d, E, k = 257, 256, 8, 2
+    gen = torch.Generator("cuda").manual_seed(4)
+    x = torch.randn(T, d, generator=gen, device="cuda").bfloat16()
+    Wg = (torch.randn(d, E, generator=gen, device="cuda") / 16).bfloat16()
+    shape = (T, d, 256, E, k)
+    idx, gate, logits = moe.moe_route(shape, x, Wg, want_logits=True)
+    s_idx, s_gate = moe.moe_route_scored(shape, logits, moe.MoeScoring())
+    assert torch.equal(idx, s_idx)
+    assert float((gate - s_gate).abs().max()) <= 1e-6
