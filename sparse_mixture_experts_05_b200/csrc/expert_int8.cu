@@ -13,13 +13,22 @@
 // of A and 256 rows of B, written by TMA with the 128-byte swizzle.  A K, an
 // output width or a row count that ends inside a box reads zeros there.
 //
-// Work is cut along K (the integers' sum does not depend on its order): the units
-// are (tile, 128 values of K), tile-major, and every CTA takes an equal run
-// of them.  A run that covers a whole tile writes its output; one that covers a part
-// stores its int32 sums in the workspace and counts its units on the tile's counter,
-// and whoever counts last adds the other parts and writes the output.  Nobody
-// waits for another CTA, the result is the same whoever comes last, and the few
-// tiles of a decode batch still load every SM alike.
+// Tiles go to single CTAs (stream_kernel, 128 rows) or to CTA pairs (pair_kernel,
+// 256 rows); plan_of() has the rule and what was measured.
+//
+// The few tiles of a small batch may be cut along K, because the integers' sum does
+// not depend on its order: the units are (tile, 128 values of K), tile-major, and
+// every CTA takes an equal run of them.  A run that covers a whole tile writes its
+// output; one that covers a part stores its int32 sums in the workspace and counts
+// its units on the tile's counter, and whoever counts last adds the parts and
+// writes the output.  Nobody waits for another CTA, the result is the same whoever
+// comes last, and every SM reads the same share of the weights.
+//
+// What bounds them: a small batch the weights' bytes (16 tokens at d = 4096, d_ff =
+// 14336, 8 experts: 147 + 79 us for 0.94 + 0.47 GB, 6.4 and 5.9 TB/s); a large one the
+// tensor cores under the power limit (4096 tokens: 700 + 340 us, 2.75 and 2.83 Pop/s);
+// many small experts both, with rows padded to 128 (2051 tokens, 64 experts, d =
+// 2048, d_ff = 1424, top-6: 97 + 68 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -27,7 +36,6 @@
 
 #include "common.cuh"
 #include "expert_int8.cuh"
-#include "expert_math.cuh"
 #include "int8_rows.cuh"
 #include "sm100.cuh"
 #include "tma_map.cuh"
@@ -49,7 +57,7 @@ constexpr int kEpiWarps = 8;                        // two for each 32 rows of a
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxE = 512;
 constexpr int kMaxGrid = 160;                       // CTAs at most (bounds the workspace)
-constexpr int kEpiBufBytes = 2048;                  // 32 rows x 32 bf16
+constexpr int kEpiBufBytes = 2048;                  // 16 rows x 64 bf16
 constexpr int kEpiScaleBytes = 512;                 // channel scales of a warp's columns
 constexpr int kEpiBytes = kEpiWarps * (kEpiBufBytes + kEpiScaleBytes);
 constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + kEpiBytes + 1024;
@@ -65,37 +73,38 @@ struct Params {
     int* err;
     uint64_t timeout_ns;
     int E, R, K, n_out;
-    int tile_cols;            // output columns of a tile (128 or 256)
-    int part_rows;            // rows of a slot: the most a tile (pair: a CTA's tile) can have
+    int tile_cols;            // pairs: output columns of a tile (128 or 256)
+    int part_rows;            // rows of a slot: the most a tile can have
     int group_m;              // m-tiles per rasterisation group
     int stall_after;
+    int may_cut;              // tiles may be cut along K
+    int cut_units;            // see Run
+    int a_rows;               // rows of an A box
 };
 
-// Exclusive prefix over the experts of their m-tiles of `rows` rows, by one warp.
-// Offsets are held to 0 .. R, so that no tile lies outside the R rows.
+// Offsets, held to 0 .. R so that no tile lies outside the R rows, and the exclusive
+// prefix over the experts of their m-tiles of `rows` rows.  All threads of the CTA.
 __device__ __forceinline__ void tile_prefix(const int32_t* offsets, int E, int R, int rows,
-                                            int* s_off, int* s_mt, int lane) {
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < E) {
-            lo = min(max(offsets[e], 0), R);
-            hi = min(max(offsets[e + 1], 0), R);
-            s_off[e] = lo;
-            if (e == E - 1) s_off[E] = hi;
-        }
-        const int mine = (max(0, hi - lo) + rows - 1) / rows;
-        int incl = mine;
+                                            int* s_off, int* s_mt) {
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) s_off[e] = min(max(offsets[e], 0), R);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int carry = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            const int mine = e < E ? (max(0, s_off[e + 1] - s_off[e]) + rows - 1) / rows : 0;
+            int incl = mine;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += o;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            if (e < E) s_mt[e] = carry + incl - mine;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (e < E) s_mt[e] = carry + incl - mine;
-        carry += __shfl_sync(0xffffffffu, incl, 31);
+        if (lane == 0) s_mt[E] = carry;
     }
-    if (lane == 0) s_mt[E] = carry;
 }
 
 struct Tile {
@@ -104,10 +113,11 @@ struct Tile {
 
 // Tile t of the expert-major order.  Within an expert the m-tiles are walked in
 // groups of `group_m`, column by column, m fastest, so that tiles which run together share
-// weight slices and a group's rows stay in L2 for all columns.  `e` is a cursor
-// that only moves forward: tiles are asked for in ascending order.
+// weight slices and a group's rows stay in L2 for all columns.  `e` is a cursor:
+// the tiles asked for mostly ascend.
 __device__ __forceinline__ Tile locate(int t, int& e, const int* s_mt, const int* s_off,
                                        int n_tiles, int tile_cols, int tile_rows, int group_m) {
+    while (t < n_tiles * s_mt[e]) --e;
     while (t >= n_tiles * s_mt[e + 1]) ++e;
     const int local = t - n_tiles * s_mt[e];
     const int mt = s_mt[e + 1] - s_mt[e];
@@ -127,7 +137,7 @@ __device__ __forceinline__ Tile locate(int t, int& e, const int* s_mt, const int
 // Eight warps: warp (q, h) takes rows 32 q .. 32 q + 31 of the tile (the TMEM lanes
 // it may read) and half h of its output columns, 64 (gate/up) or 128 (down).
 struct Epi {
-    uint8_t* buf;    // staging of one 32 x 32 bf16 block
+    uint8_t* buf;    // staging of one 16 x 64 bf16 block
     float* scales;   // channel scales of this warp's columns: 64 + 64, or 128
     int q, h, lane;
 };
@@ -139,52 +149,62 @@ __device__ __forceinline__ Epi make_epi(uint8_t* base, int warp, int lane) {
                warp & 3, w >> 2, lane};
 }
 
-// This lane's four of the warp's channel scales; x0: the warp's first output column.
-// Called before the wait for the accumulator, which then covers the load.
+// What a warp reads of a tile from memory: four channel scales and the row scale for
+// every lane.  Loaded a tile ahead.
+struct TileScales {
+    float4 channel;
+    float row;
+};
+
+// x0: the warp's first output column; row0 .. row0 + rows - 1: its rows.
 template <bool kSwiGLU, typename P>
-__device__ __forceinline__ float4 load_scales(const P& p, int e, int x0, int lane) {
+__device__ __forceinline__ TileScales load_scales(const P& p, int e, int x0, int row0, int rows,
+                                                  int lane) {
+    TileScales s;
     const float* src = kSwiGLU && lane >= 16 ? p.scale_b : p.scale_a;
     const int col = x0 + 4 * (kSwiGLU ? lane & 15 : lane);
-    if (col >= p.n_out) return make_float4(0.f, 0.f, 0.f, 0.f);
-    return __ldg(reinterpret_cast<const float4*>(src + (int64_t)e * p.n_out + col));
+    s.channel = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < p.n_out)
+        s.channel = __ldg(reinterpret_cast<const float4*>(src + (int64_t)e * p.n_out + col));
+    s.row = lane < rows ? __ldg(p.row_scale + row0 + lane) : 0.0f;
+    return s;
 }
 
-// Slot of a worker's part of a tile: the worker's run of units starts (which = 0)
-// or ends (1) in the tile.  Within a slot, 4 columns of all rows lie together.
+// A part of a tile's sums over K: int32 [rows][256].  A worker (CTA) has two slots,
+// for the tile that its run of units starts in (which = 0) and the one it ends in (1).
 __device__ __forceinline__ uint4* part_slot(uint4* slots, int worker, int which, int rows) {
     return slots + ((int64_t)(2 * worker + which) * rows) * (kAccCols / 4);
 }
 
-// The other workers' sums of a tile (first .. last except self, `step` slots pairs
-// apart); none if last < first.
+// The workers that hold parts of a tile.
 struct Parts {
-    uint4* slots;
-    int first, last, self, step, rows, row;
+    int first, last;
     bool first_is_tail;  // worker `first` holds the tile at the end of its run
 };
 
 // Workers owning units [lo, hi) of `units` dealt evenly to `active` workers.
-__device__ __forceinline__ void find_parts(Parts& parts, int64_t lo, int64_t hi, int64_t units,
-                                           int64_t active) {
+__device__ __forceinline__ Parts find_parts(int64_t lo, int64_t hi, int64_t units,
+                                            int64_t active) {
+    Parts parts;
     parts.first = (int)(((lo + 1) * active - 1) / units);
     parts.last = (int)((hi * active - 1) / units);
     parts.first_is_tail = units * parts.first / active < lo;
+    return parts;
 }
 
 // Stores this lane's row of the sums in TMEM columns [c0, c1) to `slot`.
-__device__ __forceinline__ void store_part(uint4* slot, uint32_t taddr, int c0, int c1, int rows,
-                                           int row, bool valid) {
+__device__ __forceinline__ void store_part(uint4* slot, uint32_t taddr, int c0, int c1, int row,
+                                           bool valid) {
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32cols(taddr + c, r);
+    for (int c = c0; c < c1; c += 16) {
+        uint32_t r[16];
+        tmem_ld_16cols(taddr + c, r);
         tmem_ld_wait();
         if (valid) {
-            uint4* dst = slot + (int64_t)(c >> 2) * rows + row;
+            uint4* dst = slot + row * (kAccCols / 4) + (c >> 2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                __stcg(dst + (int64_t)j * rows,
-                       make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]));
+            for (int j = 0; j < 4; ++j)
+                __stcg(dst + j, make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]));
         }
     }
 }
@@ -201,108 +221,230 @@ __device__ __forceinline__ bool count_part(int* cnt, int done, int all, int lane
     return before + done == all;
 }
 
-// r[j] = the tile's int32 sums of 32 columns of this lane's row.
-__device__ __forceinline__ void load_sums(uint32_t taddr, int c, uint32_t (&r)[32],
-                                          const Parts& parts, bool valid) {
-    tmem_ld_32cols(taddr + c, r);
-    tmem_ld_wait();
-    if (valid) {
-        for (int w = parts.first; w <= parts.last; ++w) {
-            if (w == parts.self) continue;
-            const uint4* slot = part_slot(parts.slots, w * parts.step,
-                                          w == parts.first && parts.first_is_tail ? 1 : 0,
-                                          parts.rows) + (int64_t)(c >> 2) * parts.rows + parts.row;
+// Four columns of one row summed over all parts (`at`: their place in a slot).
+__device__ __forceinline__ int4 sum_parts(uint4* slots, const Parts& parts, int rows, int at) {
+    int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll 2
+    for (int w = parts.first; w <= parts.last; ++w) {
+        const uint4 v = __ldcg(
+            part_slot(slots, w, w == parts.first && parts.first_is_tail ? 1 : 0, rows) + at);
+        sum.x += (int)v.x;
+        sum.y += (int)v.y;
+        sum.z += (int)v.z;
+        sum.w += (int)v.w;
+    }
+    return sum;
+}
+
+// float(sum) * row scale * channel scale of two neighbouring columns.
+__device__ __forceinline__ float2 scaled(int s0, int s1, float2 rs, float2 channel) {
+    const float2 f = make_float2(__int2float_rn(s0), __int2float_rn(s1));
+    return __fmul2_rn(__fmul2_rn(f, rs), channel);
+}
+
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// SiLU(a) b = a b / (1 + 2^(-a log2 e)) in two columns at once: both special-function
+// results are within two ulps and the exponent's rounding moves the power by
+// |a| 2^-24, far below h's rounding to bf16.  Below a = -87 the divisor passes
+// 2^126 and the quotient is flushed to 0 (its true value is under |a| 2^-126).  The
+// epilogue is what bounds the gate/up product at short K, and this form has 6
+// instructions an element where silu_times has about 16.
+__device__ __forceinline__ float2 silu_times2(float2 a, float2 b) {
+    constexpr float kNegLog2e = -1.4426950408889634f;
+    const float2 x = __fmul2_rn(a, make_float2(kNegLog2e, kNegLog2e));
+    const float2 d = __fadd2_rn(make_float2(exp2_ftz(x.x), exp2_ftz(x.y)), make_float2(1.f, 1.f));
+    return __fmul2_rn(__fmul2_rn(a, make_float2(rcp_ftz(d.x), rcp_ftz(d.y))), b);
+}
+
+// Output columns [x0, x0 + ncols) of the warp's 32 rows (`rows` of them exist; y0
+// is the first): sums from the accumulator's columns from c0 (and, kSwiGLU, c0 +
+// b_off for the up product) of this lane's row, scaled by rs and the warp's channel
+// scales.  64 columns are packed at a time and turned in shared memory, 16 rows
+// after 16, so that eight lanes store 128 consecutive bytes of a row: whole cache lines
+// (32-byte pieces cost the down product of many small experts 10 us of 90).
+template <bool kSwiGLU>
+__device__ __forceinline__ void write_output(const Params& p, const Epi& ep, uint32_t taddr, int c0,
+                                             int b_off, int x0, int ncols, int y0, int rows,
+                                             float rs) {
+    const int lane = ep.lane;
+    const float2 rs2 = make_float2(rs, rs);
+    // 16-byte piece j of staged row r lies at piece j ^ (r % 8): no bank conflicts
+    uint8_t* put = ep.buf + (lane & 15) * 128;
+    const int put_sw = lane & 7;
+    const int piece = lane & 7, r0 = lane >> 3;
+    __nv_bfloat16* dst = p.out + (int64_t)(y0 + r0) * p.n_out + x0 + piece * 8;
+    uint32_t ra[16], rb[16];
+    tmem_ld_16cols(taddr + c0, ra);
+    if constexpr (kSwiGLU) tmem_ld_16cols(taddr + c0 + b_off, rb);
+#pragma unroll 1
+    for (int b = 0; b < ncols; b += 64) {
+        uint32_t packed[32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = b + 16 * i;
+            const float2* sa = reinterpret_cast<const float2*>(ep.scales + c);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint4 v = __ldcg(slot + (int64_t)j * parts.rows);
-                r[4 * j] += v.x;
-                r[4 * j + 1] += v.y;
-                r[4 * j + 2] += v.z;
-                r[4 * j + 3] += v.w;
+                float2 o = scaled((int)ra[2 * j], (int)ra[2 * j + 1], rs2, sa[j]);
+                if constexpr (kSwiGLU)
+                    o = silu_times2(o, scaled((int)rb[2 * j], (int)rb[2 * j + 1], rs2, sa[32 + j]));
+                packed[8 * i + j] = pack_bf16x2(o.x, o.y);
             }
+            if (c + 16 < ncols) {  // the next sums, on their way while these are stored
+                tmem_ld_16cols(taddr + c0 + c + 16, ra);
+                if constexpr (kSwiGLU) tmem_ld_16cols(taddr + c0 + b_off + c + 16, rb);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if ((lane >> 4) == half) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(put + ((j ^ put_sw) << 4)) = make_uint4(
+                        packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+            }
+            __syncwarp();
+            if (b + piece * 8 < ncols) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 4 + r0;
+                    if (half * 16 + r < rows)
+                        *reinterpret_cast<uint4*>(dst + (int64_t)(half * 16 + i * 4) * p.n_out +
+                                                  b) =
+                            *reinterpret_cast<const uint4*>(ep.buf + r * 128 +
+                                                            ((piece ^ (r & 7)) << 4));
+                }
+            }
+            __syncwarp();
         }
     }
 }
 
-// r[j] = float(sum) * row scale * channel scale, for 32 columns.
-__device__ __forceinline__ void scale_32(uint32_t (&r)[32], float rs, const float* s) {
-    const float4* s4 = reinterpret_cast<const float4*>(s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float4 c = s4[j];
-        r[4 * j] = __float_as_uint(__int2float_rn((int)r[4 * j]) * rs * c.x);
-        r[4 * j + 1] = __float_as_uint(__int2float_rn((int)r[4 * j + 1]) * rs * c.y);
-        r[4 * j + 2] = __float_as_uint(__int2float_rn((int)r[4 * j + 2]) * rs * c.z);
-        r[4 * j + 3] = __float_as_uint(__int2float_rn((int)r[4 * j + 3]) * rs * c.w);
-    }
-}
-
-// Output columns [x0, x0 + ncols) of one row a lane: sums from the accumulator's
-// columns from c0 (and, kSwiGLU, c0 + b_off for the up product), scaled by rs and
-// the warp's channel scales.  When all 32 rows of the warp belong to the expert
-// (`tma`), 32 x 32 blocks leave as TMA stores through the staging buffer;
-// otherwise rows are stored one by one.
-template <bool kSwiGLU>
-__device__ __forceinline__ void write_output(const Params& p, const CUtensorMap* map,
-                                             const Epi& ep, uint32_t taddr, int c0, int b_off,
-                                             int x0, int ncols, int64_t grow, int y0, bool valid,
-                                             bool tma, float rs, const Parts& parts) {
-    const int lane = ep.lane;
+// The same for a tile whose sums lie in parts in the workspace: a lane takes four
+// columns of a row, so that all parts' loads are in flight together.  `rs` is lane
+// r's row scale; `prow` the warp's first row in a slot.
+// kBatch steps of rows have their loads issued together.
+template <bool kSwiGLU, int kBatch>
+__device__ __forceinline__ void write_parts(const Params& p, const Epi& ep, const Parts& parts,
+                                            int c0, int b_off, int x0, int ncols, int y0, int prow,
+                                            int rows, float rs) {
+    constexpr int kQuads = kSwiGLU ? 16 : 32;  // lanes a row takes
+    constexpr int kStep = 32 / kQuads;         // rows of the warp at a time
+    const int quad = min(ep.lane & (kQuads - 1), ncols / 4 - 1);
+    const bool mine = (ep.lane & (kQuads - 1)) == quad;
+    rows = min(rows, 32);
+    const float4 sa = reinterpret_cast<const float4*>(ep.scales)[quad];
+    const float4 sb = reinterpret_cast<const float4*>(ep.scales)[kSwiGLU ? 16 + quad : quad];
 #pragma unroll 1
-    for (int c = 0; c < ncols; c += 32) {
-        const int n = ncols - c;
-        uint32_t ra[32];
-        load_sums(taddr, c0 + c, ra, parts, valid);
-        scale_32(ra, rs, ep.scales + c);
-        if constexpr (kSwiGLU) {
-            uint32_t rb[32];
-            load_sums(taddr, c0 + b_off + c, rb, parts, valid);
-            scale_32(rb, rs, ep.scales + 64 + c);
+    for (int r0 = ep.lane / kQuads; r0 - ep.lane / kQuads < rows; r0 += kStep * kBatch) {
+        int4 a[kBatch], b[kBatch];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                ra[j] = __float_as_uint(
-                    silu_times(__uint_as_float(ra[j]), __uint_as_float(rb[j])));
+        for (int i = 0; i < kBatch; ++i) {
+            const int at = (prow + min(r0 + i * kStep, rows - 1)) * (kAccCols / 4) + (c0 >> 2) + quad;
+            a[i] = sum_parts(p.part, parts, p.part_rows, at);
+            if constexpr (kSwiGLU) b[i] = sum_parts(p.part, parts, p.part_rows, at + (b_off >> 2));
         }
-        uint32_t packed[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            packed[j] = pack_bf16x2(__uint_as_float(ra[2 * j]), __uint_as_float(ra[2 * j + 1]));
-        if (tma) {
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-            uint8_t* rowp = ep.buf + lane * 64;
-            const int sw = (lane >> 1) & 3;  // 64-byte swizzle: chunk ^= address bits 7..8
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(rowp + ((j ^ sw) << 4)) =
-                    make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2],
-                               packed[4 * j + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_2d(map, ep.buf, x0 + c, y0);
-                bulk_commit_group();
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kStep;
+            const float row = __shfl_sync(0xffffffffu, rs, r & 31);
+            const float2 rs2 = make_float2(row, row);
+            float2 lo = scaled(a[i].x, a[i].y, rs2, make_float2(sa.x, sa.y));
+            float2 hi = scaled(a[i].z, a[i].w, rs2, make_float2(sa.z, sa.w));
+            if constexpr (kSwiGLU) {
+                lo = silu_times2(lo, scaled(b[i].x, b[i].y, rs2, make_float2(sb.x, sb.y)));
+                hi = silu_times2(hi, scaled(b[i].z, b[i].w, rs2, make_float2(sb.z, sb.w)));
             }
-        } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + grow * p.n_out + x0 + c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (8 * j < n)
-                    dst[j] = make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2],
-                                        packed[4 * j + 3]);
+            if (mine && r < rows)
+                *reinterpret_cast<uint2*>(p.out + (int64_t)(y0 + r) * p.n_out + x0 + 4 * quad) =
+                    make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
         }
     }
+    __syncwarp();
 }
+
+// The work of CTA `me` of `grid`: whole tiles me, me + grid, ..., or, where `may_cut`
+// and these would leave the busiest CTA more than `cut_units` units above the average,
+// an equal run of the units (tile, 128 values of K).  Storing and adding parts
+// costs about 7 us and 0.2 us for each routed row, a unit about 0.5 us, which is what
+// the launcher puts into cut_units.  Measured at d = 4096, d_ff = 14336, 8 experts, top-2,
+// whole / cut, us: gate/up product of 1 token 44 / 44, of 16 tokens 151 / 147, of 64
+// 153 / 165; down product of 1 token 50 / 28, of 16 79 / 86, of 64 80 / 104.
+// Of a run, the parts of tiles at its two ends come first, so that whoever adds a
+// tile's parts has whole tiles to hide that behind.
+struct Run {
+    int64_t u, u0, u1, skip, units, active;
+    int kb_count, step;
+    int t, kb0, kb1;  // the current tile and its part
+
+    __device__ __forceinline__ Run(int me, int grid, int tiles, int kbs, bool may_cut,
+                                   int cut_units) {
+        kb_count = kbs;
+        units = (int64_t)tiles * kbs;
+        active = min((int64_t)grid, units);
+        const int64_t rounds = (tiles + grid - 1) / grid;
+        if (!may_cut || (rounds * kbs - cut_units) * grid <= units) {
+            u0 = (int64_t)me * kbs;
+            u1 = units;
+            skip = (int64_t)(grid - 1) * kbs;
+        } else {
+            u0 = me < active ? units * me / active : 0;
+            u1 = me < active ? units * (me + 1) / active : 0;
+            skip = 0;
+        }
+        u = u0;
+        step = 0;
+    }
+    __device__ __forceinline__ bool next() {
+        if (step == 0) {  // the part at the start, if the run starts inside a tile
+            step = 1;
+            kb0 = (int)(u0 % kb_count);
+            if (u0 < u1 && kb0 != 0) {
+                t = (int)(u0 / kb_count);
+                kb1 = (int)min((int64_t)kb_count, kb0 + (u1 - u0));
+                u = u0 + kb1 - kb0;
+                return true;
+            }
+        }
+        if (step == 1) {  // the part at the end
+            step = 2;
+            kb1 = (int)(u1 % kb_count);
+            if (u < u1 && kb1 != 0) {
+                t = (int)(u1 / kb_count);
+                kb0 = 0;
+                return true;
+            }
+        }
+        // the whole tiles in between
+        if (u + kb_count > u1) return false;
+        t = (int)(u / kb_count);
+        kb0 = 0;
+        kb1 = kb_count;
+        u += kb_count + skip;
+        return true;
+    }
+    __device__ __forceinline__ bool starts() const { return (int64_t)t * kb_count + kb0 == u0; }
+};
 
 // ------------------------------------------------------------------ the kernel
-// Roles (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer,
-// warps 2..9 epilogue.  Four stages of 48 KB; two TMEM accumulators,
+// Roles (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer, the
+// others epilogue.  Four stages of 48 KB; two TMEM accumulators,
 // so that a tile's epilogue overlaps the next tile's products.
 template <bool kSwiGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                  const __grid_constant__ CUtensorMap tmB1,
-                  const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Params p) {
+                  const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -329,26 +471,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_map(&tmA);
         tma_prefetch_map(&tmB0);
         if (kSwiGLU) tma_prefetch_map(&tmB1);
-        tma_prefetch_map(&tmOut);
     }
     if (warp == 1) {
         tmem_alloc(&tmem_slot, kTmemCols);
         tmem_relinquish();
     }
     grid_dependency_wait();
-    if (warp == 0) tile_prefix(p.offsets, p.E, p.R, kBM, s_off, s_mt, lane);
+    tile_prefix(p.offsets, p.E, p.R, kBM, s_off, s_mt);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = tmem_slot;
 
-    const int n_tiles = (p.n_out + p.tile_cols - 1) / p.tile_cols;
+    constexpr int kTileCols = kSwiGLU ? kAccCols / 2 : kAccCols;  // output columns of a tile
+    const int n_tiles = (p.n_out + kTileCols - 1) / kTileCols;
     const int kb_count = (p.K + kBK - 1) / kBK;
-    const int64_t units = (int64_t)s_mt[p.E] * n_tiles * kb_count;
-    const int64_t active = min((int64_t)gridDim.x, units);
-    const int64_t me = blockIdx.x;
-    const int64_t u0 = me < active ? units * me / active : 0;
-    const int64_t u1 = me < active ? units * (me + 1) / active : 0;
+    Run run(blockIdx.x, gridDim.x, s_mt[p.E] * n_tiles, kb_count, p.may_cut != 0,
+            p.cut_units);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -356,13 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0, issued = 0, e = 0;
             uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
             bool ok = true;
-            for (int64_t u = u0; u < u1 && ok;) {
-                const int t = (int)(u / kb_count);
-                int kb = (int)(u - (int64_t)t * kb_count);
-                const int kb1 = (int)min((int64_t)kb_count, kb + (u1 - u));
-                const Tile ti = locate(t, e, s_mt, s_off, n_tiles, p.tile_cols, kBM, p.group_m);
-                u += kb1 - kb;
-                for (; kb < kb1; ++kb) {
+            while (ok && run.next()) {
+                const Tile ti = locate(run.t, e, s_mt, s_off, n_tiles, kTileCols, kBM,
+                                       p.group_m);
+                for (int kb = run.kb0; kb < run.kb1; ++kb) {
                     if (p.stall_after >= 0 && issued >= p.stall_after) {
                         ok = false;  // test hook: behave like a producer that died
                         break;
@@ -374,13 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* sA = smem + stage * kStageBytes;
                     uint8_t* sB = sA + kABytes;
-                    mbar_arrive_expect_tx(&full_bar[stage], kStageBytes);
+                    mbar_arrive_expect_tx(&full_bar[stage], p.a_rows * kBK + 2 * kBHalf);
+                    // rows of W1 and of W3, or two halves of W2's
                     tma_load_3d(sB, &tmB0, &full_bar[stage], kb * kBK, ti.n0, ti.e);
-                    if (kSwiGLU)
-                        tma_load_3d(sB + kBHalf, &tmB1, &full_bar[stage], kb * kBK, ti.n0, ti.e);
-                    else
-                        tma_load_3d(sB + kBHalf, &tmB0, &full_bar[stage], kb * kBK,
-                                    ti.n0 + kAccCols / 2, ti.e);
+                    tma_load_3d(sB + kBHalf, kSwiGLU ? &tmB1 : &tmB0, &full_bar[stage], kb * kBK,
+                                kSwiGLU ? ti.n0 : ti.n0 + kAccCols / 2, ti.e);
                     tma_load_2d(sA, &tmA, &full_bar[stage], kb * kBK, ti.row0);
                     issued_mask |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -406,10 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t u = u0; u < u1 && ok;) {
-                const int first = (int)(u % kb_count);
-                const int kb1 = (int)min((int64_t)kb_count, first + (u1 - u));
-                u += kb1 - first;
+            while (ok && run.next()) {
                 if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, p.timeout_ns) || s_abort) {
                     record_error(p.err, kDeviceTimeoutBase | kRoleMma);
                     ok = false;
@@ -417,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + acc * kAccCols;
-                for (int kb = first; kb < kb1; ++kb) {
+                for (int kb = run.kb0; kb < run.kb1; ++kb) {
                     if (!stage_wait(&full_bar[stage], phase, p.timeout_ns, s_abort)) {
                         record_error(p.err, kDeviceTimeoutBase | kRoleMma);
                         ok = false;
@@ -429,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kBK / 32; ++kk)
                         tc_mma_s8(d_tmem, adesc0 + soff + kk * (32 >> 4),
                                   bdesc0 + soff + kk * (32 >> 4), idesc,
-                                  kb != first || kk != 0);
+                                  kb != run.kb0 || kk != 0);
                     tc_commit(&empty_bar[stage]);
                     if (++stage == kStages) {
                         stage = 0;
@@ -449,23 +580,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------- epilogue
         const Epi ep = make_epi(smem + kStages * kStageBytes, warp, lane);
-        constexpr int kCols = kSwiGLU ? 64 : 128;  // output columns of a warp
-        const int row = ep.q * 32 + lane;
+        constexpr int kCols = kTileCols / 2;  // output columns of a warp
+        constexpr int b_off = kSwiGLU ? kAccCols / 2 : 0;
+        const int c0 = ep.h * kCols;
+        const int row0 = ep.q * 32;
         int acc = 0, e = 0;
         uint32_t acc_phase = 0;
-        for (int64_t u = u0; u < u1;) {
-            const int t = (int)(u / kb_count);
-            const int kb = (int)(u - (int64_t)t * kb_count);
-            const int done = (int)min((int64_t)kb_count - kb, u1 - u);
-            const bool at_start = u == u0;
-            u += done;
-            const Tile ti = locate(t, e, s_mt, s_off, n_tiles, p.tile_cols, kBM, p.group_m);
-            const int x0 = ti.n0 + ep.h * kCols;
-            const int ncols = min(kCols, p.n_out - x0);
-            const bool valid = row < ti.rows;
-            const int64_t grow = (int64_t)ti.row0 + row;
-            const float4 sc = load_scales<kSwiGLU>(p, ti.e, x0, lane);
-            const float rs = valid ? __ldg(p.row_scale + grow) : 0.0f;
+        Tile ti{};
+        TileScales sc{};
+        bool more = run.next();
+        if (more) {
+            ti = locate(run.t, e, s_mt, s_off, n_tiles, kTileCols, kBM, p.group_m);
+            sc = load_scales<kSwiGLU>(p, ti.e, ti.n0 + c0, ti.row0 + row0, ti.rows - row0, lane);
+        }
+        while (more) {
             const bool got = mbar_wait(&acc_full[acc], acc_phase, p.timeout_ns);
             if (!got || s_abort) {
                 if (!got) record_error(p.err, kDeviceTimeoutBase | kRoleEpilogue);
@@ -473,38 +601,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after_sync();
-            reinterpret_cast<float4*>(ep.scales)[lane] = sc;
+            reinterpret_cast<float4*>(ep.scales)[lane] = sc.channel;
             __syncwarp();
-            const uint32_t taddr = tmem_base + acc * kAccCols + ((uint32_t)(ep.q * 32) << 16);
-            const int c0 = ep.h * kCols;
-            const int b_off = kSwiGLU ? kAccCols / 2 : 0;
-            Parts parts{p.part, 0, -1, (int)me, 1, p.part_rows, row, false};
-            // warp-uniform: this warp has rows and columns
-            bool write = ep.q * 32 < ti.rows && ncols > 0;
-            if (write && done < kb_count) {
-                // a part of the tile's K: store the sums, count, and finish if last
-                uint4* slot = part_slot(p.part, (int)me, at_start ? 0 : 1, p.part_rows);
-                store_part(slot, taddr, c0, c0 + ncols, p.part_rows, row, valid);
-                if (kSwiGLU)
-                    store_part(slot, taddr, b_off + c0, b_off + c0 + ncols, p.part_rows, row,
-                               valid);
-                write = count_part(p.cnt + (int64_t)t * kEpiWarps + warp - 2, done, kb_count, lane);
-                const int64_t lo = (int64_t)t * kb_count;
-                if (write) find_parts(parts, lo, lo + kb_count, units, active);
+            const Tile now = ti;
+            const float rs = sc.row;
+            const int t = run.t, done = run.kb1 - run.kb0;
+            const bool starts = run.starts();
+            more = run.next();
+            if (more) {  // the next tile's scales load behind this one's work
+                ti = locate(run.t, e, s_mt, s_off, n_tiles, kTileCols, kBM, p.group_m);
+                sc = load_scales<kSwiGLU>(p, ti.e, ti.n0 + c0, ti.row0 + row0, ti.rows - row0,
+                                          lane);
             }
-            if (write)
-                write_output<kSwiGLU>(p, &tmOut, ep, taddr, c0, b_off, x0, ncols, grow,
-                                      ti.row0 + ep.q * 32, valid, ep.q * 32 + 32 <= ti.rows, rs,
-                                      parts);
+            const uint32_t taddr = tmem_base + acc * kAccCols + ((uint32_t)row0 << 16);
+            const int x0 = now.n0 + c0;
+            const int ncols = min(kCols, p.n_out - x0);
+            if (row0 < now.rows && ncols > 0) {  // warp-uniform: this warp has rows and columns
+                if (done == kb_count) {
+                    write_output<kSwiGLU>(p, ep, taddr, c0, b_off, x0, ncols, now.row0 + row0,
+                                          now.rows - row0, rs);
+                } else {
+                    // a part of the tile's K: store the sums, count, and finish if last
+                    uint4* slot =
+                        part_slot(p.part, blockIdx.x, starts ? 0 : 1, p.part_rows);
+                    const bool valid = row0 + lane < now.rows;
+                    store_part(slot, taddr, c0, c0 + ncols, row0 + lane, valid);
+                    if (kSwiGLU)
+                        store_part(slot, taddr, b_off + c0, b_off + c0 + ncols, row0 + lane,
+                                          valid);
+                    if (count_part(p.cnt + (int64_t)t * kEpiWarps + warp - 2, done, kb_count,
+                                   lane)) {
+                        const int64_t lo = (int64_t)t * kb_count;
+                        const Parts parts = find_parts(lo, lo + kb_count, run.units, run.active);
+                        if (now.rows - row0 <= 2)
+                            write_parts<kSwiGLU, 1>(p, ep, parts, c0, b_off, x0, ncols,
+                                                    now.row0 + row0, row0, now.rows - row0, rs);
+                        else
+                            write_parts<kSwiGLU, 4>(p, ep, parts, c0, b_off, x0, ncols,
+                                                    now.row0 + row0, row0, now.rows - row0, rs);
+                    }
+                }
+            }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[acc]);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
-        // the staging buffers outlive every store that reads them
-        if (lane == 0) bulk_wait_group<0>();
-        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -525,11 +668,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // columns are a(0..63) b(0..63) a(64..127) b(64..127).  An expert's last rows
 // are a tile like the others (its MMA takes as long with 128 rows as with 256).
 //
-// Tiles are dealt round-robin while they fill whole rounds of the pairs: tiles that
-// run together then share weight slices and rows in L2 (a run of tiles per pair, as
-// in the single-CTA kernel, re-reads each slice from DRAM for every m-tile once the
-// pairs' slices together exceed L2).  The tiles of the last, partial round are cut
-// along K over all pairs, as above.
+// Tiles are dealt round-robin: tiles that run together then share weight slices and
+// rows in L2 (a run of tiles per pair, as in the single-CTA kernel, re-reads each
+// slice from DRAM for every m-tile once the pairs' slices together exceed L2).  Cutting
+// the last, partial round along K as above measured slower: storing and adding parts
+// of 256 rows took about 25 us, more than a whole tile of K = 3584 (layer of 1024
+// tokens, d = 1024, d_ff = 3584: 58 + 28 us against 30 + 18).
 //
 // Synchronisation: both CTAs' loads count on the leader's full barriers; the
 // leader's MMA thread commits consumed stages and finished accumulators to both
@@ -541,56 +685,11 @@ constexpr int kPairStages = 6;
 constexpr int kPairBBytes = (kAccCols / 2) * kBK;          // 16 KB: this CTA's 128 B rows
 constexpr int kPairStageBytes = kABytes + kPairBBytes;     // 32 KB
 constexpr size_t kPairSmemBytes = (size_t)kPairStages * kPairStageBytes + kEpiBytes + 1024;
-constexpr int kMaxPairs = kMaxGrid / 2;
-
-// The work of pair `me`: whole tiles me, me + pairs, ... of the full rounds, then
-// units [u0, u1) of the remaining tiles.  next() steps through both.
-struct PairWork {
-    int pairs, rounds, round, kb_count, rest0;  // rest0: first tile of the partial round
-    int64_t u, u0, u1, units;
-    // the current segment
-    int t, kb0, kb1;
-
-    __device__ __forceinline__ PairWork(int me, int n_pairs, int tiles, int kbs) {
-        pairs = n_pairs;
-        rounds = tiles / n_pairs;
-        round = 0;
-        kb_count = kbs;
-        rest0 = rounds * n_pairs;
-        units = (int64_t)(tiles - rest0) * kbs;
-        // fewer units than pairs: one each, for as many pairs as there are units
-        const int64_t active = min((int64_t)n_pairs, units);
-        u0 = me < active ? units * me / active : 0;
-        u1 = me < active ? units * (me + 1) / active : 0;
-        u = u0;
-        t = me - n_pairs;
-    }
-    __device__ __forceinline__ bool next() {
-        if (round < rounds) {
-            ++round;
-            t += pairs;
-            kb0 = 0;
-            kb1 = kb_count;
-            return true;
-        }
-        if (u >= u1) return false;
-        const int r = (int)(u / kb_count);
-        kb0 = (int)(u - (int64_t)r * kb_count);
-        kb1 = (int)min((int64_t)kb_count, kb0 + (u1 - u));
-        t = rest0 + r;
-        u += kb1 - kb0;
-        return true;
-    }
-    __device__ __forceinline__ bool whole() const { return kb1 - kb0 == kb_count; }
-    // whether the current part is the first of this pair's units
-    __device__ __forceinline__ bool at_start() const { return u - (kb1 - kb0) == u0; }
-};
 
 template <bool kSwiGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                const __grid_constant__ CUtensorMap tmB1,
-                const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Params p) {
+                const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -621,14 +720,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch_map(&tmA);
         tma_prefetch_map(&tmB0);
         if (kSwiGLU) tma_prefetch_map(&tmB1);
-        tma_prefetch_map(&tmOut);
     }
     if (warp == 1) {
         tmem_alloc_pair(&tmem_slot, kTmemCols);
         tmem_relinquish_pair();
     }
     grid_dependency_wait();
-    if (warp == 0) tile_prefix(p.offsets, p.E, p.R, kPairRows, s_off, s_mt, lane);
+    tile_prefix(p.offsets, p.E, p.R, kPairRows, s_off, s_mt);
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync_all();  // the peer's barriers are initialised before anyone signals them
@@ -637,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     const int n_tiles = (p.n_out + p.tile_cols - 1) / p.tile_cols;
     const int kb_count = (p.K + kBK - 1) / kBK;
-    PairWork work(me, npairs, s_mt[p.E] * n_tiles, kb_count);
+    const int tiles = s_mt[p.E] * n_tiles;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -646,11 +744,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
             bool ok = true;
             const uint32_t leader_full0 = map_to_cta(smem_u32(&full_bar[0]), 0);
-            while (ok && work.next()) {
-                const Tile ti = locate(work.t, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows,
+            for (int t = me; t < tiles && ok; t += npairs) {
+                const Tile ti = locate(t, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows,
                                        p.group_m);
                 const int arow = ti.row0 + rank * kBM;
-                for (int kb = work.kb0; kb < work.kb1; ++kb) {
+                for (int kb = 0; kb < kb_count; ++kb) {
                     if (p.stall_after >= 0 && issued >= p.stall_after) {
                         ok = false;  // test hook: both producers stop at the same stage
                         break;
@@ -698,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            while (ok && work.next()) {
+            for (int t = me; t < tiles && ok; t += npairs) {
                 if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, p.timeout_ns) || s_abort) {
                     record_error(p.err, kDeviceTimeoutBase | kRoleMma);
                     ok = false;
@@ -709,7 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // the next stage's barrier is looked at before this stage's MMAs
                 // are issued, so that its wait overlaps them
                 bool ready = mbar_try_wait(&full_bar[stage], phase);
-                for (int kb = work.kb0; kb < work.kb1; ++kb) {
+                for (int kb = 0; kb < kb_count; ++kb) {
                     if (!ready && !stage_wait(&full_bar[stage], phase, p.timeout_ns, s_abort)) {
                         record_error(p.err, kDeviceTimeoutBase | kRoleMma);
                         ok = false;
@@ -721,13 +819,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                    ready = kb + 1 < work.kb1 && mbar_try_wait(&full_bar[stage], phase);
+                    ready = kb + 1 < kb_count && mbar_try_wait(&full_bar[stage], phase);
                     const uint64_t soff = (uint64_t)((uint32_t)(cur * kPairStageBytes) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk)
                         tc_mma_s8_pair(d_tmem, adesc0 + soff + kk * (32 >> 4),
                                        bdesc0 + soff + kk * (32 >> 4), idesc,
-                                       kb != work.kb0 || kk != 0);
+                                       (kb | kk) != 0);
                     tc_commit_pair_mc(smem_u32(&empty_bar[cur]), 0x3);
                 }
                 if (!ok) break;
@@ -743,20 +841,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------- epilogue (both CTAs)
         const Epi ep = make_epi(smem + kPairStages * kPairStageBytes, warp, lane);
         constexpr int kCols = kSwiGLU ? 64 : 128;
-        const int row = ep.q * 32 + lane;
+        const int row0 = rank * kBM + ep.q * 32;  // this warp's first row of a tile
         int acc = 0, e = 0;
         uint32_t acc_phase = 0;
         const uint32_t leader_acc_empty0 = map_to_cta(smem_u32(&acc_empty[0]), 0);
-        while (work.next()) {
-            const Tile ti = locate(work.t, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows,
-                                   p.group_m);
-            const int x0 = ti.n0 + ep.h * kCols;
-            const int ncols = min(kCols, p.n_out - x0);
-            const int row0 = rank * kBM + ep.q * 32;  // this warp's first row of the tile
-            const bool valid = row0 + lane < ti.rows;
-            const int64_t grow = (int64_t)ti.row0 + row0 + lane;
-            const float4 sc = load_scales<kSwiGLU>(p, ti.e, x0, lane);
-            const float rs = valid ? __ldg(p.row_scale + grow) : 0.0f;
+        Tile ti{};
+        TileScales sc{};
+        if (me < tiles) {
+            ti = locate(me, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows, p.group_m);
+            sc = load_scales<kSwiGLU>(p, ti.e, ti.n0 + ep.h * kCols, ti.row0 + row0,
+                                      ti.rows - row0, lane);
+        }
+        for (int t = me; t < tiles; t += npairs) {
             const bool got = mbar_wait(&acc_full[acc], acc_phase, p.timeout_ns);
             if (!got || s_abort) {
                 if (!got) record_error(p.err, kDeviceTimeoutBase | kRoleEpilogue);
@@ -764,35 +860,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after_sync();
-            reinterpret_cast<float4*>(ep.scales)[lane] = sc;
+            reinterpret_cast<float4*>(ep.scales)[lane] = sc.channel;
             __syncwarp();
-            const uint32_t taddr = tmem_base + acc * kAccCols + ((uint32_t)(ep.q * 32) << 16);
-            const int c0 = ep.h * 128;
-            // a CTA's slots: worker 2 pair + rank
-            Parts parts{p.part + (int64_t)rank * 2 * p.part_rows * (kAccCols / 4), 0, -1, me, 2,
-                        p.part_rows, row, false};
-            bool write = row0 < ti.rows && ncols > 0;
-            if (write && !work.whole()) {
-                uint4* slot = part_slot(parts.slots, 2 * me, work.at_start() ? 0 : 1, p.part_rows);
-                store_part(slot, taddr, c0, c0 + 128, p.part_rows, row, valid);
-                const int r = work.t - work.rest0;
-                write = count_part(p.cnt + ((int64_t)r * 2 + rank) * kEpiWarps + warp - 2,
-                                   work.kb1 - work.kb0, kb_count, lane);
-                if (write)
-                    find_parts(parts, (int64_t)r * kb_count, (int64_t)(r + 1) * kb_count,
-                               work.units, min((int64_t)npairs, work.units));
+            const Tile now = ti;
+            const float rs = sc.row;
+            if (t + npairs < tiles) {  // the next tile's scales load behind this one's work
+                ti = locate(t + npairs, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows,
+                            p.group_m);
+                sc = load_scales<kSwiGLU>(p, ti.e, ti.n0 + ep.h * kCols, ti.row0 + row0,
+                                          ti.rows - row0, lane);
             }
-            if (write)
-                write_output<kSwiGLU>(p, &tmOut, ep, taddr, c0, kSwiGLU ? 64 : 0, x0, ncols, grow,
-                                      ti.row0 + row0, valid, row0 + 32 <= ti.rows, rs, parts);
+            const int x0 = now.n0 + ep.h * kCols;
+            const int ncols = min(kCols, p.n_out - x0);
+            if (row0 < now.rows && ncols > 0)
+                write_output<kSwiGLU>(
+                    p, ep, tmem_base + acc * kAccCols + ((uint32_t)(ep.q * 32) << 16), ep.h * 128,
+                    kSwiGLU ? 64 : 0, x0, ncols, now.row0 + row0, now.rows - row0, rs);
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(leader_acc_empty0 + acc * (uint32_t)sizeof(uint64_t));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
-        if (lane == 0) bulk_wait_group<0>();
-        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -811,21 +900,14 @@ bool rows_map(CUtensorMap* map, const void* base, int64_t rows, int cols, int bo
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
     const uint64_t strides[1] = {(uint64_t)cols};
     const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)box_rows};
-    return make_map(map, base, 1, 2, dims, strides, box, 128);
+    return make_byte_map(map, base, 2, dims, strides, box);
 }
 
 bool weights_map(CUtensorMap* map, const void* base, int E, int n, int k, int box_rows) {
     const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E};
     const uint64_t strides[2] = {(uint64_t)k, (uint64_t)n * (uint64_t)k};
     const uint32_t box[3] = {(uint32_t)kBK, (uint32_t)box_rows, 1};
-    return make_map(map, base, 1, 3, dims, strides, box, 128);
-}
-
-bool output_map(CUtensorMap* map, const void* base, int64_t rows, int cols) {
-    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
-    const uint64_t strides[1] = {(uint64_t)cols * 2};
-    const uint32_t box[2] = {32, 32};
-    return make_map(map, base, 2, 2, dims, strides, box, 64);
+    return make_byte_map(map, base, 3, dims, strides, box);
 }
 
 // Pairs that can be resident at once (a cluster lies within one GPC); per device.
@@ -848,43 +930,87 @@ int resident_pairs() {
             (void)cudaGetLastError();
             return 0;
         }
-        cached[dev] = std::min(n, kMaxPairs);
+        cached[dev] = n;
     }
     return cached[dev];
 }
 
-// Rows from which tiles run on CTA pairs.
-constexpr int64_t kPairMinRows = 512;
+// How the rows of a call are worked on.
+//  kCut: single CTAs, tiles cut along K where that pays; kDealt: single CTAs, whole
+//  tiles; kPairs: CTA pairs, whole tiles.
+enum Plan { kCut, kDealt, kPairs };
+
+// From 512 routed rows there are enough tiles, and enough rows for parts to be dear
+// (512 tokens, d = 4096, d_ff = 14336, 8 experts, top-2: 163 us whole, 278 cut).
+// Pairs read a third fewer bytes into the SMs for the same products but pad rows to
+// 256, not 128: they win at long K, where that traffic decides, and for the gate/up
+// product only once experts have many rows.  Single / pairs, us, K and rows an
+// expert: down product 768, 240: 77 / 98; 1424, 192: 68 / 68; 3584, 256: 20 / 18;
+// 8192, 256: 96 / 84; 14336, 1024: 378 / 340; 14336, 4096: 1316 / 1230; gate/up
+// product 1024, 256: 25 / 30; 2048, 192: 97 / 101; 2048, 256: 149 / 159; 4096, 128:
+// 163 / 184; 4096, 1024: 700 / 710; 4096, 4096: 2585 / 2464.
+Plan plan_of(const moe_shape& s, int K, bool swiglu) {
+    const int64_t R = (int64_t)s.T * s.k;
+    if (R < 512) return kCut;
+    return K >= 3500 && (!swiglu || R >= (int64_t)1536 * s.E) ? kPairs : kDealt;
+}
+
+// m-tiles per group: their rows within 32 MB of the 126 MB L2, and at least 2048 rows.
+int group_of(int tile_rows, int K) {
+    return (int)std::max<int64_t>(2048 / tile_rows, (int64_t(32) << 20) / ((int64_t)tile_rows * K));
+}
 
 template <bool kSwiGLU>
-int launch_product(const moe_shape& s, const int8_t* a, const int8_t* b0, const int8_t* b1,
-                   Params p, cudaStream_t st) {
-    const int64_t R = (int64_t)s.T * s.k;
-    const bool pairs = R >= kPairMinRows;
-    CUtensorMap ma, mb0, mb1, mo;
-    const int b_rows = pairs && kSwiGLU ? 64 : 128;
-    if (!rows_map(&ma, a, R, p.K, kBM) || !weights_map(&mb0, b0, s.E, p.n_out, p.K, b_rows) ||
-        !weights_map(&mb1, b1, s.E, p.n_out, p.K, b_rows) || !output_map(&mo, p.out, R, p.n_out))
+int launch_pairs(const moe_shape& s, const int8_t* a, const int8_t* b0, const int8_t* b1, Params p,
+                 cudaStream_t st) {
+    CUtensorMap ma, mb0, mb1;
+    const int b_rows = kSwiGLU ? 64 : 128;
+    if (!rows_map(&ma, a, p.R, p.K, kBM) || !weights_map(&mb0, b0, s.E, p.n_out, p.K, b_rows) ||
+        !weights_map(&mb1, b1, s.E, p.n_out, p.K, b_rows))
         return MOE_ERR_CUDA;
-    if (pairs) {
-        // m-tiles per group: their rows within 32 MB of the 126 MB L2, and at least 8
-        p.group_m = (int)std::max<int64_t>(8, (int64_t(32) << 20) / ((int64_t)kPairRows * p.K));
-        const int n = resident_pairs<kSwiGLU>();
-        if (n <= 0) return MOE_ERR_CUDA;
-        return launch_pdl(pair_kernel<kSwiGLU>, dim3(2 * n), dim3(kThreads), kPairSmemBytes, st, ma,
-                          mb0, mb1, mo, p) == cudaSuccess
-                   ? MOE_OK
-                   : MOE_ERR_CUDA;
-    }
-    p.group_m = 1 << 20;
+    p.group_m = group_of(kPairRows, p.K);
+    const int n = resident_pairs<kSwiGLU>();
+    if (n <= 0) return MOE_ERR_CUDA;
+    return launch_pdl(pair_kernel<kSwiGLU>, dim3(2 * n), dim3(kThreads), kPairSmemBytes, st, ma,
+                      mb0, mb1, p) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+template <bool kSwiGLU>
+int launch_single(const moe_shape& s, const int8_t* a, const int8_t* b0, const int8_t* b1, Params p,
+                  bool may_cut, cudaStream_t st) {
+    // a box has as many rows as there are, in eights: rows past the tensor's end are
+    // filled with zeros at a price (5 experts' weights, 8 rows: 135 us with boxes of
+    // 128 rows, 110 with 8)
+    p.a_rows = (int)std::min<int64_t>(kBM, (p.R + 7) / 8 * 8);
+    p.may_cut = may_cut;
+    p.cut_units = 14 + 3 * p.R / 8;
+    p.part_rows = (int)std::min<int64_t>(kBM, p.R);
+    p.group_m = group_of(kBM, p.K);
+    CUtensorMap ma, mb0, mb1;
+    if (!rows_map(&ma, a, p.R, p.K, p.a_rows) ||
+        !weights_map(&mb0, b0, s.E, p.n_out, p.K, kAccCols / 2) ||
+        !weights_map(&mb1, b1, s.E, p.n_out, p.K, kAccCols / 2))
+        return MOE_ERR_CUDA;
     auto kern = stream_kernel<kSwiGLU>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)kSmemBytes))
         return MOE_ERR_CUDA;
     const int grid = std::min(kMaxGrid, device_sm_count());
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, st, ma, mb0, mb1, mo, p) ==
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, st, ma, mb0, mb1, p) ==
                    cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+template <bool kSwiGLU>
+int launch_product(const moe_shape& s, const int8_t* a, const int8_t* b0, const int8_t* b1,
+                   const Params& p, cudaStream_t st) {
+    switch (plan_of(s, p.K, kSwiGLU)) {
+        case kCut: return launch_single<kSwiGLU>(s, a, b0, b1, p, true, st);
+        case kDealt: return launch_single<kSwiGLU>(s, a, b0, b1, p, false, st);
+        default: return launch_pairs<kSwiGLU>(s, a, b0, b1, p, st);
+    }
 }
 
 }  // namespace int8gemm
@@ -892,8 +1018,6 @@ int launch_product(const moe_shape& s, const int8_t* a, const int8_t* b0, const 
 Int8Workspace int8_workspace(const moe_shape& s) {
     using namespace int8gemm;
     const size_t R = (size_t)s.T * s.k;
-    const size_t mtiles = R / kBM + std::min<size_t>(R, s.E);
-    const size_t rows = std::min<size_t>(kBM, R);
     Int8Workspace w{};
     size_t off = kWsHeaderBytes;
     auto take = [&](size_t bytes) {
@@ -901,12 +1025,18 @@ Int8Workspace int8_workspace(const moe_shape& s) {
         off = align_up(off + bytes, 256);
         return at;
     };
-    // counters: of every tile, or, on CTA pairs, of the tiles of one partial round
-    const bool pairs = (int64_t)R >= kPairMinRows;
-    w.cnt1 = take(4 * kEpiWarps * (pairs ? 2 * kMaxPairs : mtiles * ((s.d_ff + 127) / 128)));
-    w.cnt2 = take(4 * kEpiWarps * (pairs ? 2 * kMaxPairs : mtiles * ((s.d + 255) / 256)));
+    // counters of the tiles that may be cut, and two slots of parts for each CTA
+    size_t slots = 0;
+    auto counters = [&](int K, int n_out, bool swiglu) -> size_t {
+        if (plan_of(s, K, swiglu) != kCut) return 0;
+        const size_t cols = swiglu ? kAccCols / 2 : kAccCols;
+        slots = 2 * (size_t)kMaxGrid * std::min<size_t>(kBM, R) * kAccCols * 4;
+        return (R / kBM + std::min<size_t>(R, s.E)) * ((n_out + cols - 1) / cols) * kEpiWarps * 4;
+    };
+    w.cnt1 = take(counters(s.d, s.d_ff, true));
+    w.cnt2 = take(counters(s.d_ff, s.d, false));
     w.zero_bytes = off;
-    w.part = take(2 * (size_t)kMaxGrid * rows * kAccCols * 4);
+    w.part = take(slots);
     w.hs = take(R * 4);
     w.hq = take(R * s.d_ff);
     w.h = take(R * s.d_ff * 2);
@@ -935,7 +1065,6 @@ int expert_products_int8(const moe_shape& s, const int8_t* xq, const float* xs,
     p.K = s.d;
     p.n_out = s.d_ff;
     p.tile_cols = kAccCols / 2;
-    p.part_rows = (int)std::min<int64_t>(kBM, (int64_t)s.T * s.k);
     p.stall_after = stall_after;
     int rc = launch_product<true>(s, xq, w.W1, w.W3, p, stream);
     if (rc) return rc;

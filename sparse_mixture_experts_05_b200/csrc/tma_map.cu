@@ -45,9 +45,8 @@ bool make_bf16_map_3d(CUtensorMap* map, const void* base, const uint64_t (&dims)
            CUDA_SUCCESS;
 }
 
-bool make_map(CUtensorMap* map, const void* base, int element_bytes, int rank,
-              const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-              int swizzle_bytes) {
+bool make_byte_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box) {
     EncodeTiled fn = encoder();
     if (!fn || rank < 2 || rank > 3) return false;
     cuuint64_t d[3], st[2];
@@ -58,11 +57,8 @@ bool make_map(CUtensorMap* map, const void* base, int element_bytes, int rank,
         bx[i] = box[i];
         if (i + 1 < rank) st[i] = strides[i];
     }
-    return fn(map,
-              element_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), d, st,
+              bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }

@@ -13,12 +13,9 @@ namespace moe {
 bool make_bf16_map_3d(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
                       const uint64_t (&strides)[2], const uint32_t (&box)[3]);
 
-// 2-D or 3-D tensor map of 1-byte (unsigned 8-bit codes) or 2-byte (bf16) elements:
-// dims innermost first, strides (bytes) of dims 1 and 2, box extents; swizzled in shared
-// memory in rows of `swizzle_bytes` (64 or 128).  Coordinates past a dimension
-// read as zeros and are not stored.
-bool make_map(CUtensorMap* map, const void* base, int element_bytes, int rank,
-              const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-              int swizzle_bytes);
+// 2-D or 3-D tensor map of 8-bit codes: dims innermost first, strides (bytes) of
+// dims 1 and 2, box extents, 128-byte swizzle, coordinates past a dimension read as zeros.
+bool make_byte_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box);
 
 }  // namespace moe
