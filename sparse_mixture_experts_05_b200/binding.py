@@ -11,6 +11,7 @@ Shapes follow the C header: `shape = (T, d, d_ff, E, k)`.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -170,19 +171,29 @@ def status_string(status: int) -> str:
     return lib().moe_status_string(int(status)).decode()
 
 
+@functools.lru_cache(maxsize=1024)
+def _shape_of(T, d, d_ff, E, k) -> MoeShape:
+    return MoeShape(int(T), int(d), int(d_ff), int(E), int(k))
+
+
 def _shape(shape) -> MoeShape:
-    T, d, d_ff, E, k = (int(v) for v in shape)
-    return MoeShape(T, d, d_ff, E, k)
+    return _shape_of(*shape)  # passed by value: one object serves every call of a shape
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(fn: str, rc: int):
@@ -608,12 +619,32 @@ def moe_read_device_status(ws, stream=None) -> int:
 _LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _logits(t: torch.Tensor, shape) -> int:
-    T, d, d_ff, E, k = shape
-    if t.dtype not in _LOGITS_TYPES:
+def _arg(t, name: str, dtype, shape, device: int):
+    """The pointer of a checked argument (None stays None): _dev's checks, and that it lies on
+    the current device, on whose stream the work is enqueued."""
+    if t is None:
+        return None
+    if t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous() \
+            and t.get_device() == device:
+        return t.data_ptr()
+    _dev(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _given(t, name: str, like):
+    """A required argument; `like`: what says where new outputs go."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not like.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _logits(t, shape, device: int):
+    """(pointer, type code) of router logits."""
+    kind = _LOGITS_TYPES.get(t.dtype)
+    if kind is None:
         raise ValueError(f"logits must be float32 or bfloat16, got {t.dtype}")
-    _dev(t, "logits", t.dtype, (T, E))
-    return _LOGITS_TYPES[t.dtype]
+    return _arg(t, "logits", t.dtype, (shape[0], shape[3]), device), kind
 
 
 def moe_check_scoring(shape, scoring: MoeScoring) -> int:
@@ -640,16 +671,18 @@ def moe_route_scored(shape, logits, scoring: MoeScoring, bias=None, mask=None, i
     Returns (idx [T, k] int32, gate [T, k] float32); idx -1 (gate 0) marks a slot that
     no expert fills.  Only T, E and k of `shape` are used."""
     T, d, d_ff, E, k = shape
-    kind = _logits(logits, shape)
-    _dev(bias, "bias", torch.float32, (E,))
-    _dev(mask, "mask", torch.uint8, (T,))
-    idx = _new((T, k), torch.int32, logits) if idx is None else idx
-    gate = _new((T, k), torch.float32, logits) if gate is None else gate
-    _dev(idx, "idx", torch.int32, (T, k))
-    _dev(gate, "gate", torch.float32, (T, k))
+    _given(logits, "logits", logits)
+    dev = torch.cuda.current_device()
+    lp, kind = _logits(logits, shape, dev)
+    bp = _arg(bias, "bias", torch.float32, (E,), dev)
+    mp = _arg(mask, "mask", torch.uint8, (T,), dev)
+    idx = logits.new_empty((T, k), dtype=torch.int32) if idx is None else idx
+    gate = logits.new_empty((T, k), dtype=torch.float32) if gate is None else gate
     _check("moe_route_scored",
-           lib().moe_route_scored(_shape(shape), scoring, _p(logits), kind, _p(bias), _p(mask),
-                                  _p(idx), _p(gate), _stream(stream)))
+           lib().moe_route_scored(_shape(shape), scoring, lp, kind, bp, mp,
+                                  _arg(idx, "idx", torch.int32, (T, k), dev),
+                                  _arg(gate, "gate", torch.float32, (T, k), dev),
+                                  _stream(stream)))
     return idx, gate
 
 
@@ -659,30 +692,34 @@ def moe_route_scored_backward(shape, logits, scoring: MoeScoring, idx, dgate, dl
 
     `idx` is the forward call's; `dgate` [T, k] float32 the gates' gradient."""
     T, d, d_ff, E, k = shape
-    kind = _logits(logits, shape)
-    _dev(idx, "idx", torch.int32, (T, k))
-    _dev(dgate, "dgate", torch.float32, (T, k))
-    dlogits = _new((T, E), logits.dtype, logits) if dlogits is None else dlogits
-    _dev(dlogits, "dlogits", logits.dtype, (T, E))
+    _given(logits, "logits", logits)
+    dev = torch.cuda.current_device()
+    lp, kind = _logits(logits, shape, dev)
+    ip = _arg(idx, "idx", torch.int32, (T, k), dev)
+    gp = _arg(dgate, "dgate", torch.float32, (T, k), dev)
+    dlogits = torch.empty_like(logits) if dlogits is None else dlogits
     _check("moe_route_scored_backward",
-           lib().moe_route_scored_backward(_shape(shape), scoring, _p(logits), kind, _p(idx),
-                                           _p(dgate), _p(dlogits), _stream(stream)))
+           lib().moe_route_scored_backward(_shape(shape), scoring, lp, kind, ip, gp,
+                                           _arg(dlogits, "dlogits", logits.dtype, (T, E), dev),
+                                           _stream(stream)))
     return dlogits
 
 
 def moe_quantize_weights_int8(W, Wq=None, scale=None, stream=None):
     """(Wq [E, N, K] int8, scale [E, N] float32) of bf16 weights W [E, K, N]: one scale for
     each output channel.  The pairs are what moe_expert_swiglu_int8 takes as W1, W3, W2."""
-    _dev(W, "W", torch.bfloat16)
+    _given(W, "W", W)
     if W.dim() != 3:
         raise ValueError(f"W must have shape (E, K, N), got {tuple(W.shape)}")
     E, K, N = W.shape
-    Wq = _new((E, N, K), torch.int8, W) if Wq is None else Wq
-    scale = _new((E, N), torch.float32, W) if scale is None else scale
-    _dev(Wq, "Wq", torch.int8, (E, N, K))
-    _dev(scale, "scale", torch.float32, (E, N))
+    dev = torch.cuda.current_device()
+    wp = _arg(W, "W", torch.bfloat16, (E, K, N), dev)
+    Wq = W.new_empty((E, N, K), dtype=torch.int8) if Wq is None else Wq
+    scale = W.new_empty((E, N), dtype=torch.float32) if scale is None else scale
     _check("moe_quantize_weights_int8",
-           lib().moe_quantize_weights_int8(E, K, N, _p(W), _p(Wq), _p(scale), _stream(stream)))
+           lib().moe_quantize_weights_int8(E, K, N, wp, _arg(Wq, "Wq", torch.int8, (E, N, K), dev),
+                                           _arg(scale, "scale", torch.float32, (E, N), dev),
+                                           _stream(stream)))
     return Wq, scale
 
 
@@ -691,47 +728,55 @@ def moe_dispatch_int8(shape, idx, x, offsets=None, perm_tok=None, inv=None, xq=N
     """moe_dispatch whose sorted rows leave quantised: returns (offsets, perm_tok, inv,
     xq [T*k, d] int8, xs [T*k] float32)."""
     T, d, d_ff, E, k = shape
-    _dev(idx, "idx", torch.int32, (T, k))
-    _dev(x, "x", torch.bfloat16, (T, d))
-    offsets = _new((E + 1,), torch.int32, x) if offsets is None else offsets
-    perm_tok = _new((T * k,), torch.int32, x) if perm_tok is None else perm_tok
-    inv = _new((T, k), torch.int32, x) if inv is None else inv
-    xq = _new((T * k, d), torch.int8, x) if xq is None else xq
-    xs = _new((T * k,), torch.float32, x) if xs is None else xs
-    _dev(offsets, "offsets", torch.int32, (E + 1,))
-    _dev(perm_tok, "perm_tok", torch.int32, (T * k,))
-    _dev(inv, "inv", torch.int32, (T, k))
-    _dev(xq, "xq", torch.int8, (T * k, d))
-    _dev(xs, "xs", torch.float32, (T * k,))
+    _given(x, "x", x)
+    dev = torch.cuda.current_device()
+    ip = _arg(idx, "idx", torch.int32, (T, k), dev)
+    xp = _arg(x, "x", torch.bfloat16, (T, d), dev)
+    offsets = x.new_empty((E + 1,), dtype=torch.int32) if offsets is None else offsets
+    perm_tok = x.new_empty((T * k,), dtype=torch.int32) if perm_tok is None else perm_tok
+    inv = x.new_empty((T, k), dtype=torch.int32) if inv is None else inv
+    xq = x.new_empty((T * k, d), dtype=torch.int8) if xq is None else xq
+    xs = x.new_empty((T * k,), dtype=torch.float32) if xs is None else xs
     _check("moe_dispatch_int8",
-           lib().moe_dispatch_int8(_shape(shape), _p(idx), _p(x), _p(offsets), _p(perm_tok),
-                                   _p(inv), _p(xq), _p(xs), _stream(stream)))
+           lib().moe_dispatch_int8(_shape(shape), ip, xp,
+                                   _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
+                                   _arg(perm_tok, "perm_tok", torch.int32, (T * k,), dev),
+                                   _arg(inv, "inv", torch.int32, (T, k), dev),
+                                   _arg(xq, "xq", torch.int8, (T * k, d), dev),
+                                   _arg(xs, "xs", torch.float32, (T * k,), dev), _stream(stream)))
     return offsets, perm_tok, inv, xq, xs
 
 
-def _int8_weights(shape, W1, W3, W2):
+def _int8_weights(shape, W1, W3, W2, device: int):
     """Pointers of the (int8, scale) pairs W1, W3 [E, d_ff, d] and W2 [E, d, d_ff]."""
     T, d, d_ff, E, k = shape
-    out = []
-    for name, pair, n, kk in (("W1", W1, d_ff, d), ("W3", W3, d_ff, d), ("W2", W2, d, d_ff)):
-        q, s = pair
-        _dev(q, name, torch.int8, (E, n, kk))
-        _dev(s, f"{name} scale", torch.float32, (E, n))
-        out += [_p(q), _p(s)]
-    return out
+    (q1, s1), (q3, s3), (q2, s2) = W1, W3, W2
+    return (_arg(q1, "W1", torch.int8, (E, d_ff, d), device),
+            _arg(s1, "W1 scale", torch.float32, (E, d_ff), device),
+            _arg(q3, "W3", torch.int8, (E, d_ff, d), device),
+            _arg(s3, "W3 scale", torch.float32, (E, d_ff), device),
+            _arg(q2, "W2", torch.int8, (E, d, d_ff), device),
+            _arg(s2, "W2 scale", torch.float32, (E, d), device))
 
 
-def _int8_expert_args(shape, xq, xs, offsets, o, ws):
+def _ws_arg(ws, device: int):
+    """(pointer, bytes) of a workspace: a uint8 tensor of any length."""
+    return _arg(ws, "ws", torch.uint8, ws.shape, device), ws.numel()
+
+
+def _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws):
     T, d, d_ff, E, k = shape
     R = T * k
-    _dev(xq, "xq", torch.int8, (R, d))
-    _dev(xs, "xs", torch.float32, (R,))
-    _dev(offsets, "offsets", torch.int32, (E + 1,))
-    o = _new((R, d), torch.bfloat16, xq) if o is None else o
-    ws = workspace(moe_expert_swiglu_int8_workspace_bytes(shape), xq.device) if ws is None else ws
-    _dev(o, "o", torch.bfloat16, (R, d))
-    _dev(ws, "ws", torch.uint8)
-    return o, ws
+    _given(xq, "xq", xq)
+    dev = torch.cuda.current_device()
+    o = xq.new_empty((R, d), dtype=torch.bfloat16) if o is None else o
+    if ws is None:
+        ws = workspace(moe_expert_swiglu_int8_workspace_bytes(shape), xq.device)
+    args = (_arg(xq, "xq", torch.int8, (R, d), dev), _arg(xs, "xs", torch.float32, (R,), dev),
+            _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
+            *_int8_weights(shape, W1, W3, W2, dev), _arg(o, "o", torch.bfloat16, (R, d), dev),
+            *_ws_arg(ws, dev))
+    return args, o, ws
 
 
 def moe_expert_swiglu_int8(shape, xq, xs, offsets, W1, W3, W2, o=None, ws=None, stream=None):
@@ -739,35 +784,32 @@ def moe_expert_swiglu_int8(shape, xq, xs, offsets, W1, W3, W2, o=None, ws=None, 
 
     W1, W3, W2 are the (int8, scale) pairs of moe_quantize_weights_int8.  Returns
     (o [T*k, d] bfloat16, ws)."""
-    o, ws = _int8_expert_args(shape, xq, xs, offsets, o, ws)
-    weights = _int8_weights(shape, W1, W3, W2)
+    args, o, ws = _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws)
     _check("moe_expert_swiglu_int8",
-           lib().moe_expert_swiglu_int8(_shape(shape), _p(xq), _p(xs), _p(offsets), *weights,
-                                        _p(o), _p(ws), ws.numel(), _stream(stream)))
+           lib().moe_expert_swiglu_int8(_shape(shape), *args, _stream(stream)))
     return o, ws
 
 
 def moe_expert_swiglu_int8_stall_test(shape, xq, xs, offsets, W1, W3, W2, stall_after: int,
                                       timeout_ns: int, o=None, ws=None, stream=None):
-    o, ws = _int8_expert_args(shape, xq, xs, offsets, o, ws)
-    weights = _int8_weights(shape, W1, W3, W2)
+    args, o, ws = _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws)
     _check("moe_expert_swiglu_int8_stall_test",
-           lib().moe_expert_swiglu_int8_stall_test(_shape(shape), _p(xq), _p(xs), _p(offsets),
-                                                   *weights, _p(o), _p(ws), ws.numel(),
-                                                   int(stall_after), int(timeout_ns),
-                                                   _stream(stream)))
+           lib().moe_expert_swiglu_int8_stall_test(_shape(shape), *args, int(stall_after),
+                                                   int(timeout_ns), _stream(stream)))
     return o, ws
 
 
 def moe_combine_bf16(shape, o, inv, gate, y=None, stream=None):
+    """moe_combine over bfloat16 expert outputs o [T*k, d]."""
     T, d, d_ff, E, k = shape
-    _dev(o, "o", torch.bfloat16, (T * k, d))
-    _dev(inv, "inv", torch.int32, (T, k))
-    _dev(gate, "gate", torch.float32, (T, k))
-    y = _new((T, d), torch.bfloat16, o) if y is None else y
-    _dev(y, "y", torch.bfloat16, (T, d))
-    _check("moe_combine_bf16", lib().moe_combine_bf16(_shape(shape), _p(o), _p(inv), _p(gate),
-                                                      _p(y), _stream(stream)))
+    _given(o, "o", o)
+    dev = torch.cuda.current_device()
+    y = o.new_empty((T, d)) if y is None else y
+    _check("moe_combine_bf16",
+           lib().moe_combine_bf16(_shape(shape), _arg(o, "o", torch.bfloat16, (T * k, d), dev),
+                                  _arg(inv, "inv", torch.int32, (T, k), dev),
+                                  _arg(gate, "gate", torch.float32, (T, k), dev),
+                                  _arg(y, "y", torch.bfloat16, (T, d), dev), _stream(stream)))
     return y
 
 
@@ -777,19 +819,19 @@ def moe_forward_int8(shape, x, logits, scoring: MoeScoring, W1, W3, W2, route_bi
     logits [T, E] (float32, as of moe_route, or bfloat16).  W1, W3, W2 are the
     (int8, scale) pairs of moe_quantize_weights_int8."""
     T, d, d_ff, E, k = shape
-    _dev(x, "x", torch.bfloat16, (T, d))
-    kind = _logits(logits, shape)
-    _dev(route_bias, "route_bias", torch.float32, (E,))
-    _dev(mask, "mask", torch.uint8, (T,))
-    weights = _int8_weights(shape, W1, W3, W2)
-    y = _new((T, d), torch.bfloat16, x) if y is None else y
+    _given(x, "x", x)
+    _given(logits, "logits", logits)
+    dev = torch.cuda.current_device()
+    lp, kind = _logits(logits, shape, dev)
+    y = torch.empty_like(x) if y is None else y
     ws = workspace(moe_forward_int8_workspace_bytes(shape), x.device) if ws is None else ws
-    _dev(y, "y", torch.bfloat16, (T, d))
-    _dev(idx_out, "idx_out", torch.int32, (T, k))
-    _dev(gate_out, "gate_out", torch.float32, (T, k))
-    _dev(ws, "ws", torch.uint8)
     _check("moe_forward_int8",
-           lib().moe_forward_int8(_shape(shape), _p(x), _p(logits), kind, scoring, _p(route_bias),
-                                  _p(mask), *weights, _p(y), _p(idx_out), _p(gate_out), _p(ws),
-                                  ws.numel(), _stream(stream)))
+           lib().moe_forward_int8(_shape(shape), _arg(x, "x", torch.bfloat16, (T, d), dev), lp, kind,
+                                  scoring, _arg(route_bias, "route_bias", torch.float32, (E,), dev),
+                                  _arg(mask, "mask", torch.uint8, (T,), dev),
+                                  *_int8_weights(shape, W1, W3, W2, dev),
+                                  _arg(y, "y", torch.bfloat16, (T, d), dev),
+                                  _arg(idx_out, "idx_out", torch.int32, (T, k), dev),
+                                  _arg(gate_out, "gate_out", torch.float32, (T, k), dev),
+                                  *_ws_arg(ws, dev), _stream(stream)))
     return y
