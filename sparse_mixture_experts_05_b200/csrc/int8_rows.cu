@@ -80,12 +80,14 @@ __device__ __forceinline__ uint32_t max_abs16(const uint4& a, const uint4& b, ui
     return max_abs2(max_abs2(max_abs2(max_abs2(m, b.x), b.y), b.z), b.w);
 }
 
-// Largest of both halves over the block (every thread returns it).
-__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* s_max) {
+// Largest of both halves over the row's threads, a warp or the block (every thread
+// returns it).
+template <bool kWarpRow>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* s_max) {
     uint32_t one = max(m & 0xffffu, m >> 16);
     one = __reduce_max_sync(kAll, one);
+    if (kWarpRow) return one;
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return one;
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = one;
     __syncthreads();
     uint32_t all = 0;
@@ -93,23 +95,28 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* s_max) {
     return all;
 }
 
-// One block quantises one row of `units` x 16 values; NU > 0: the row stays in
-// registers (NU units a thread), 0: it is read twice (the second time from L2).
-// kScatter: row t = blockIdx.x goes to its k sorted rows; otherwise to row t
-// itself, if t < *n_rows.
-template <int NU, bool kScatter>
+// A block, or (kWarpRow) a warp, quantises one row of `units` x 16 values; NU > 0:
+// the row stays in registers (NU units a thread), 0: it is read twice (the second time
+// from L2).  kScatter: row t goes to its k sorted rows; otherwise row r to row r
+// itself, if r < *map.  Both directions are whole vectors of consecutive bytes, so the
+// memory bounds them: rows of 14336 values, 8192 of them, 54 us (6.5 TB/s).
+template <int NU, bool kScatter, bool kWarpRow>
 __global__ void __launch_bounds__(256)
-    quantize_kernel(const uint4* __restrict__ x, int units, const int32_t* __restrict__ map, int k,
-                    uint4* __restrict__ xq, float* __restrict__ xs, uint32_t* zero,
-                    int64_t zero_words) {
+    quantize_kernel(const uint4* __restrict__ x, int64_t rows, int units,
+                    const int32_t* __restrict__ map, int k, uint4* __restrict__ xq,
+                    float* __restrict__ xs, uint32_t* zero, int64_t zero_words) {
     __shared__ uint32_t s_max[8];
     grid_dependency_wait();
-    const int64_t row = blockIdx.x;
+    const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+    const int threads = kWarpRow ? 32 : blockDim.x;
+    const int64_t row = kWarpRow ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                                 : (int64_t)blockIdx.x;
     if (kScatter) {
-        for (int64_t i = row * blockDim.x + threadIdx.x; i < zero_words;
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < zero_words;
              i += (int64_t)gridDim.x * blockDim.x)
             zero[i] = 0u;
-    } else if (row >= __ldg(map)) {
+        if (kWarpRow && row >= rows) return;
+    } else if (row >= min(rows, (int64_t)__ldg(map))) {
         return;
     }
     const uint4* src = x + row * units * 2;
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(256)
     if constexpr (NU > 0) {
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
-            const int u = threadIdx.x + n * blockDim.x;
+            const int u = tid + n * threads;
             v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
             if (u < units) {
                 v[n][0] = __ldg(src + 2 * u);
@@ -128,41 +135,48 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int n = 0; n < NU; ++n) m = max_abs16(v[n][0], v[n][1], m);
     } else {
-        for (int u = threadIdx.x; u < units; u += blockDim.x)
+        for (int u = tid; u < units; u += threads)
             m = max_abs16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), m);
     }
-    const Quant q = make_quant(block_max(m, s_max));
+    const Quant q = make_quant(row_max<kWarpRow>(m, s_max));
     const int copies = kScatter ? k : 1;
     for (int s = 0; s < copies; ++s) {
         const int64_t dst = kScatter ? (int64_t)__ldg(map + row * k + s) : row;
         if (dst < 0) continue;
-        if (threadIdx.x == 0) xs[dst] = q.scale;
+        if (tid == 0) xs[dst] = q.scale;
         if constexpr (NU > 0) {
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
-                const int u = threadIdx.x + n * blockDim.x;
+                const int u = tid + n * threads;
                 if (u < units) xq[dst * units + u] = quantize16(v[n][0], v[n][1], q);
             }
         } else {
-            for (int u = threadIdx.x; u < units; u += blockDim.x)
+            for (int u = tid; u < units; u += threads)
                 xq[dst * units + u] = quantize16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), q);
         }
     }
 }
 
+// A warp a row up to 2048 values, when there are rows for it: less than 8 warps of a
+// block would have work, or wait for the others (32792 rows of 768: 20 us by blocks).
 template <bool kScatter>
 int launch_quantize(const void* x, int64_t rows, int cols, const int32_t* map, int k, int8_t* xq,
                     float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t st) {
     const int units = cols / 16;
-    const int threads = std::min(256, (units + 31) / 32 * 32);
-    const int per = (units + threads - 1) / threads;
-    auto kern = per <= 1   ? quantize_kernel<1, kScatter>
-                : per <= 2 ? quantize_kernel<2, kScatter>
-                : per <= 4 ? quantize_kernel<4, kScatter>
-                           : quantize_kernel<0, kScatter>;
-    return launch_pdl(kern, dim3((unsigned)rows), dim3(threads), 0, st,
-                      static_cast<const uint4*>(x), units, map, k, reinterpret_cast<uint4*>(xq),
-                      xs, zero, zero_words) == cudaSuccess
+    const bool by_warp = units <= 128 && rows >= 1024;
+    const int threads = by_warp ? 256 : std::min(256, (units + 31) / 32 * 32);
+    const int per = by_warp ? (units + 31) / 32 : (units + threads - 1) / threads;
+    const int64_t blocks = by_warp ? (rows + 7) / 8 : rows;
+    auto kern = by_warp ? (per <= 1   ? quantize_kernel<1, kScatter, true>
+                           : per <= 2 ? quantize_kernel<2, kScatter, true>
+                                      : quantize_kernel<4, kScatter, true>)
+                        : (per <= 1   ? quantize_kernel<1, kScatter, false>
+                           : per <= 2 ? quantize_kernel<2, kScatter, false>
+                           : per <= 4 ? quantize_kernel<4, kScatter, false>
+                                      : quantize_kernel<0, kScatter, false>);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(threads), 0, st,
+                      static_cast<const uint4*>(x), rows, units, map, k,
+                      reinterpret_cast<uint4*>(xq), xs, zero, zero_words) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -249,9 +263,10 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ token lists
 // The index kernel of the dispatch for more experts: the same cluster of C CTAs and the
 // same contiguous runs of slots per warp, with a counter for each (warp, expert) in
-// shared memory.  Thread e scans expert e's counters over the CTA's 32 warps and
-// reads the other CTAs' totals through distributed shared memory; a scan over
-// the experts gives their first rows.  Stable, deterministic, no atomics on positions.
+// shared memory.  The warps take the experts in turn and scan an expert's counters
+// over the CTA's 32 warps; thread e reads the other CTAs' totals of expert e through
+// distributed shared memory, and a scan over the experts gives their first rows.
+// Stable, deterministic, no atomics on positions.  perm_tok may be null.
 constexpr int kIndexThreads = 1024;
 constexpr int kIndexWarps = 32;
 constexpr int kMaxE = 512;
@@ -272,48 +287,54 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 }
 
 __global__ void __launch_bounds__(kIndexThreads, 1)
-    index_many_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int k,
+    index_many_kernel(const int32_t* __restrict__ idx, int n, int E, int k,
                       int32_t* __restrict__ offsets, int32_t* __restrict__ perm_tok,
                       int32_t* __restrict__ inv) {
-    extern __shared__ int s_pos[];  // [32][E]: counts, then next positions
-    __shared__ int s_total[kMaxE];
+    extern __shared__ int s_pos[];  // [32][E + 1]: counts, then positions within the CTA
+    __shared__ int s_total[kMaxE];  // this CTA's rows of each expert
+    __shared__ int s_base[kMaxE];   // the expert's first row in this CTA
     __shared__ int s_warp[kIndexWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)sm100::cluster_ctarank();
     const int C = (int)cluster_ctas();
-    int* pos = s_pos + warp * E;
+    const int pitch = E | 1;  // odd: an expert's 32 counters lie in 32 banks
+    int* pos = s_pos + warp * pitch;
     for (int e = lane; e < E; e += 32) pos[e] = 0;
     __syncwarp();
     grid_dependency_wait();
-    const int64_t per_warp = ((n + kIndexWarps * C - 1) / (kIndexWarps * C) + 31) / 32 * 32;
-    const int64_t j0 = min(n, (int64_t)(rank * kIndexWarps + warp) * per_warp);
-    const int64_t j1 = min(n, j0 + per_warp);
+    const int nwarps = kIndexWarps * C;
+    const int per_warp = ((n + nwarps - 1) / nwarps + 31) / 32 * 32;
+    const int j0 = min(n, (rank * kIndexWarps + warp) * per_warp);
+    const int j1 = min(n, j0 + per_warp);
     const unsigned lt = (1u << lane) - 1u;
-    for (int64_t base = j0; base < j1; base += 32 * kBatch) {
-        int ids[kBatch];
+    const bool one_batch = per_warp <= 32 * kBatch;  // pass 2 reuses pass 1's ids
+    int ids[kBatch];
+    for (int base = j0; base < j1; base += 32 * kBatch) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int64_t j = base + u * 32 + lane;
+            const int j = base + u * 32 + lane;
             ids[u] = j < j1 ? __ldg(idx + j) : -1;
+            if (ids[u] >= E) ids[u] = -1;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (base + u * 32 >= j1) break;
-            const bool valid = ids[u] >= 0 && ids[u] < E;
-            const unsigned same = __match_any_sync(kAll, valid ? ids[u] : -1);
-            if (valid && (same & lt) == 0) pos[ids[u]] += __popc(same);
+            const unsigned same = __match_any_sync(kAll, ids[u]);
+            if (ids[u] >= 0 && (same & lt) == 0) pos[ids[u]] += __popc(same);
             __syncwarp();
         }
     }
     __syncthreads();
-    int mine = 0;  // rows of expert `tid` in this CTA
-    if (tid < E) {
-        for (int w = 0; w < kIndexWarps; ++w) {
-            const int c = s_pos[w * E + tid];
-            s_pos[w * E + tid] = mine;
-            mine += c;
+    for (int e = warp; e < E; e += kIndexWarps) {  // lane = warp of the CTA
+        const int c = s_pos[lane * pitch + e];
+        int incl = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(kAll, incl, off);
+            if (lane >= off) incl += o;
         }
-        s_total[tid] = mine;
+        s_pos[lane * pitch + e] = incl - c;
+        if (lane == 31) s_total[e] = incl;
     }
     sm100::cluster_sync_all();
     int before = 0, total = 0;
@@ -333,38 +354,39 @@ __global__ void __launch_bounds__(kIndexThreads, 1)
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int start = incl - total;
-    for (int w = 0; w < warp; ++w) start += s_warp[w];
-    if (rank == 0) {
-        if (tid < E) offsets[tid] = start;
-        if (tid == E - 1) offsets[E] = start + total;
-    }
     if (tid < E) {
-        for (int w = 0; w < kIndexWarps; ++w) s_pos[w * E + tid] += start + before;
+        int start = incl - total;
+        for (int w = 0; w < warp; ++w) start += s_warp[w];
+        s_base[tid] = start + before;
+        if (rank == 0) {
+            offsets[tid] = start;
+            if (tid == E - 1) offsets[E] = start + total;
+        }
     }
     __syncthreads();
-    for (int64_t base = j0; base < j1; base += 32 * kBatch) {
-        int ids[kBatch];
+    for (int base = j0; base < j1; base += 32 * kBatch) {
+        if (!one_batch) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int64_t j = base + u * 32 + lane;
-            ids[u] = j < j1 ? __ldg(idx + j) : -1;
+            for (int u = 0; u < kBatch; ++u) {
+                const int j = base + u * 32 + lane;
+                ids[u] = j < j1 ? __ldg(idx + j) : -1;
+                if (ids[u] >= E) ids[u] = -1;
+            }
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (base + u * 32 >= j1) break;
-            const int64_t j = base + u * 32 + lane;
-            const bool valid = ids[u] >= 0 && ids[u] < E;
-            const unsigned same = __match_any_sync(kAll, valid ? ids[u] : -1);
-            if (valid) {
-                const int p = pos[ids[u]] + __popc(same & lt);
-                perm_tok[p] = (int)(j / k);
-                inv[j] = p;
-            } else if (j < j1) {
-                inv[j] = -1;
+            const int j = base + u * 32 + lane;
+            const int e = ids[u];
+            const unsigned same = __match_any_sync(kAll, e);
+            int p = -1;
+            if (e >= 0) {
+                p = pos[e] + s_base[e] + __popc(same & lt);
+                if (perm_tok) perm_tok[p] = j / k;
             }
+            if (j < j1) inv[j] = p;
             __syncwarp();
-            if (valid && (same & lt) == 0) pos[ids[u]] += __popc(same);
+            if (e >= 0 && (same & lt) == 0) pos[e] += __popc(same);
             __syncwarp();
         }
     }
@@ -424,9 +446,9 @@ int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* 
     const int64_t n = (int64_t)s.T * s.k;
     int C = 1;
     while (C < kMaxCluster && n > (int64_t)C * kIndexWarps * kSlotsPerWarp) C *= 2;
-    const int smem = kIndexWarps * s.E * 4;
+    const int smem = kIndexWarps * (s.E + 1) * 4;
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(index_many_kernel),
-                             kIndexWarps * kMaxE * 4))
+                             kIndexWarps * (kMaxE + 1) * 4))
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C);
@@ -442,7 +464,7 @@ int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, n, (int)s.E, (int)s.k, offsets,
+    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, (int)n, (int)s.E, (int)s.k, offsets,
                               perm_tok, inv) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;

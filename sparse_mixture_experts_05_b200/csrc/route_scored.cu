@@ -9,23 +9,32 @@
 //     S = the k largest choices left (ties: the lower index)
 //     gate_i = scale * s_i / sum_{j in S} s_j     (or scale * s_i)
 //
-// One warp works on one row.  Lane L holds the V consecutive experts from
-// L * V, and choices are compared as unsigned integers in the floats' order, which
-// makes the largest of 32 lanes one redux instruction.
+// Forward: LPR lanes (8, 16 or 32) work on a row, so 4, 2 or 1 rows share a warp's
+// instructions; a lane holds V experts, and a group is P whole lanes (rows whose groups
+// do not fill their lanes are padded with -inf).  A choice becomes a 32-bit key, its
+// value in the upper 23 bits and the expert's number in the lower 9, so that minimum
+// and maximum move both at once and a lower number wins a tie.  The value is the distance
+// from the row's largest choice in fixed point, 2^-23 of a range of 4 (biased choices)
+// or 32 (logits); bf16 logits without a bias keep their 16 bits instead.  Each lane
+// sorts its best KL >= k keys; a group's value comes from the first two of its lanes'
+// lists; then the lanes' lists are merged in pairs, KL against KL, which leaves the
+// row's best in every lane and the best of all that fell out in `out`.
 //
 // Three attempts, each taken only where the one before could not tell two experts
 // (or the last kept and first dropped group) apart:
-//  1. packed: the low bits of a choice's key give way to the expert's number, so that
-//     one redux yields both and no lane has to be asked who won; each lane sorts its V
-//     keys once, and a selected one is shifted out.  Rows whose neighbours in the selected
-//     order lie within the lost bits and the error of a float32 score go on (under 1 in
-//     100 of 256 biased sigmoids; bf16 logits without a bias lose no bits).
-//  2. candidates: four more of them are taken, and each lane forms one candidate's
-//     choice in float64; ranking them decides, unless the last may lie as high as
-//     the k-th.
-//  3. all choices in float64: where the groups are too close, or the second
-//     attempt does not decide, or a biased softmax needs its sum in float64.
+//  1. the keys: rows whose neighbours in the selected order have the same value, or
+//     differ by less than the error of a float32 score, go on.
+//  2. the KL best in float64, one a lane: their ranking decides, unless `out` may lie
+//     as high as the k-th.
+//  3. all choices in float64 by the whole warp: where the groups are too close, the
+//     second attempt does not decide, a biased softmax needs its sum in float64, or
+//     a selected choice lies beyond the keys' range (too few live experts among it).
 // So the selection is that of float64 scores.
+//
+// What bounds it: instructions.  16384 rows of 256 experts, sigmoid, bias, 4 of 8
+// groups, top-8 (18 MB, 3 us at the memory's rate) take 24 us, 12 of them the keys and lists
+// of about 400 instructions a row and the rest scores, groups and the last warps' third
+// attempts; a row a warp with rounds of warp-wide maxima took 1000 instructions and 31 us.
 //
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,22 +49,25 @@ namespace moe {
 namespace scored {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8;  // rows in work per block
+constexpr int kWarps = 8;         // backward: rows in work per block
+constexpr int kForwardWarps = 4;  // forward: warps per block
 // Blocks an SM holds: as many as V values a lane leave registers for.
 constexpr int blocks_per_sm(int V) { return V <= 2 ? 6 : V == 4 ? 5 : V == 8 ? 4 : 2; }
-constexpr int kExtra = 4;  // candidates beyond the first one left out (second attempt)
 
 struct Args {
     int T, E, k;
     int sigmoid, renorm;
     int n_group, group_size, topk_group, group_top;
-    int group_lanes;  // lanes of one group when groups are whole lanes, a power of two; else 0
+    int group_lanes;  // forward: P, lanes of one group
+    int lane_size;    // forward: experts a lane takes of its group, at most V
+    int aligned;      // forward: expert i is value i of the row's lanes (no padding inside)
     int biased;       // choices are scores plus a bias; otherwise logits order them
     int sums;         // groups are valued by a sum of two choices
     int whole_keys;   // without a bias, keys leave their low bits zero (bf16 logits)
-    float lost;       // what a packed key may lose, relative to its value
+    float steps;      // key values per unit of choice (2^23 / range)
     int slots;        // k, rounded up to a power of two
-    int vec;          // rows can be read in vectors
+    int unit;         // bytes a row can be read in at a time (16, 8, 4 or 2)
+    int vec;          // backward: rows can be read in vectors
     float scale;
 };
 
@@ -150,9 +162,6 @@ __device__ __forceinline__ float warp_max_float(float v) { return from_key(warp_
 
 // exp(l - m) with l <= m; 1 where they are equal (both infinite among it).
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
-__device__ __forceinline__ double exp_below(double l, double m) {
-    return l == m ? 1.0 : exp(l - m);
-}
 __device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 __device__ __forceinline__ double sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
 
@@ -179,112 +188,122 @@ __device__ __forceinline__ void merge_top2(K& b1, K& b2, K o1, K o2) {
 }
 
 // ------------------------------------------------------------------ third attempt
-// Selects the row's k experts: lane r < k returns the expert of slot r, or -1.  All
-// choices in float64, whole keys; without a bias the logits order the experts.
-template <int V>
-__device__ __noinline__ int select_double(const float (&l)[V], const Args& a, const float* bias,
-                                          int lane) {
+__device__ __noinline__ double score_double(double x, bool is_sigmoid, double m, double inv) {
+    // one exponential for both kinds: it is the bulk of this path's instructions, which
+    // nearly always have to be fetched when a row needs them
+    const double e = exp(is_sigmoid ? -x : (x == m ? 0.0 : x - m));
+    return is_sigmoid ? 1.0 / (1.0 + e) : e * inv;
+}
+
+// Selects the row's k experts by the whole warp: lane r < k returns the expert of slot
+// r, or -1.  All choices in float64, in `c` (E values of shared memory); without a
+// bias the logits order the experts.  Rolled loops: few rows come here, and a kernel's
+// last warp waits for them (8 us a row with the loops unrolled, 2 without).
+template <typename L>
+__device__ __noinline__ int select_double(const L* __restrict__ row, const Args& a,
+                                          const float* __restrict__ bias, int lane, double* c) {
     typedef unsigned long long K;
-    const int i0 = lane * V;
     double m = 0.0, inv = 1.0;
     if (!a.sigmoid && (a.biased || a.sums)) {
-        double sum;
-        softmax_stats<double, V>(l, m, sum);
-        inv = 1.0 / sum;
-    }
-    auto score = [&](double x) { return a.sigmoid ? sigmoid(x) : exp_below(x, m) * inv; };
-    K key[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        key[j] = 0;
-        if (l[j] > -INFINITY) {
-            double c = (double)l[j];
-            if (a.biased) c = score(c) + (double)__ldg(bias + i0 + j);
-            if (c > -INFINITY) key[j] = ordered(c);
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int i = lane; i < a.E; i += 32) top = fmaxf(top, to_float(row[i]));
+        m = (double)from_key(__reduce_max_sync(kAll, ordered(top)));
+        double sum = 0.0;
+#pragma unroll 1
+        for (int i = lane; i < a.E; i += 32) {
+            const float f = to_float(row[i]);
+            if (f > -INFINITY) sum += score_double((double)f, false, m, 1.0);
         }
+        inv = 1.0 / warp_sum(sum);
     }
+#pragma unroll 1
+    for (int i0 = lane; i0 < a.E; i0 += 128) {
+        double v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // (an expert past E has score 1 or inv, and no place)
+            const int i = i0 + 32 * j;
+            v[j] = i < a.E ? (double)to_float(row[i]) : m;
+        }
+        if (a.biased) {
+            double b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const double x = v[j];
+                b[j] = exp(a.sigmoid ? -x : (x == m ? 0.0 : x - m));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + 32 * j;
+                if (v[j] > -INFINITY)
+                    v[j] = (a.sigmoid ? 1.0 / (1.0 + b[j]) : b[j] * inv) +
+                           (i < a.E ? (double)__ldg(bias + i) : 0.0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + 32 * j < a.E) c[i0 + 32 * j] = v[j] > -INFINITY ? v[j] : -INFINITY;
+    }
+    __syncwarp();
     if (a.n_group > 1) {
         K value = 0;
+#pragma unroll 1
         for (int g = 0; g < a.n_group; ++g) {
             K t1 = 0, t2 = 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const unsigned in = (unsigned)(i0 + j - g * a.group_size);
-                merge_top2(t1, t2, in < (unsigned)a.group_size ? key[j] : (K)0, (K)0);
-            }
+#pragma unroll 1
+            for (int i = g * a.group_size + lane; i < (g + 1) * a.group_size; i += 32)
+                merge_top2(t1, t2, c[i] > -INFINITY ? ordered(c[i]) : (K)0, (K)0);
             const K m1 = warp_max(t1);
             const bool many = __popc(__ballot_sync(kAll, t1 == m1)) > 1;
             const K m2 = warp_max(t1 == m1 && !many ? t2 : t1);
             if (lane == g && m1 != 0) {
                 value = m1;
                 if (a.sums) {
-                    const double v1 = from_key(m1), v2 = m2 != 0 ? from_key(m2) : 0.0;
-                    value = ordered(a.biased ? v1 + v2
-                                             : score(v1) + (m2 != 0 ? score(v2) : 0.0));
+                    double v1 = from_key(m1), v2 = m2 != 0 ? from_key(m2) : 0.0;
+                    if (!a.biased) {
+                        v1 = score_double(v1, a.sigmoid, m, inv);
+                        if (m2 != 0) v2 = score_double(v2, a.sigmoid, m, inv);
+                    }
+                    value = ordered(v1 + v2);
                 }
             }
         }
         int rank = 0;
+#pragma unroll 1
         for (int g = 0; g < a.n_group; ++g) {
             const K o = __shfl_sync(kAll, value, g);
             rank += o > value || (o == value && g < lane);
         }
         const unsigned keep = __ballot_sync(kAll, lane < a.n_group && rank < a.topk_group);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (i0 + j < a.E && !((keep >> ((i0 + j) / a.group_size)) & 1u)) key[j] = 0;
+#pragma unroll 1
+        for (int i = lane; i < a.E; i += 32)
+            if (!((keep >> (i / a.group_size)) & 1u)) c[i] = -INFINITY;
+        __syncwarp();
     }
     int mine = -1;
+#pragma unroll 1
     for (int r = 0; r < a.k; ++r) {
-        K head = 0;
-        int at = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (key[j] > head) {
-                head = key[j];
-                at = j;
+        double head = -INFINITY;
+        int at = 0x7fffffff;
+#pragma unroll 4
+        for (int i = lane; i < a.E; i += 32)
+            if (c[i] > head) {
+                head = c[i];
+                at = i;
             }
-        const K best = warp_max(head);
+        const K key = head > -INFINITY ? ordered(head) : (K)0;
+        const K best = warp_max(key);
         if (best == 0) break;
-        const int owner = __ffs(__ballot_sync(kAll, head == best)) - 1;
-        const int chosen = __shfl_sync(kAll, i0 + at, owner);
+        const int chosen = (int)__reduce_min_sync(kAll, key == best ? (unsigned)at : 0xffffffffu);
         if (lane == r) mine = chosen;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (i0 + j == chosen) key[j] = 0;
+        if (lane == (chosen & 31)) c[chosen] = -INFINITY;
+        __syncwarp();
     }
+    __syncwarp();
     return mine;
 }
 
-// ------------------------------------------------------------------ packed attempt
-template <int V>
-struct Packed {
-    static constexpr int kBits = V == 1 ? 5 : V == 2 ? 6 : V == 4 ? 7 : V == 8 ? 8 : 9;
-    static constexpr uint32_t kLow = (1u << kBits) - 1u;
-};
-
-// Descending, by Batcher's odd-even merge network.
-template <int V>
-__device__ __forceinline__ void sort_descending(uint32_t (&k)[V]) {
-#pragma unroll
-    for (int p = 1; p < V; p *= 2) {
-#pragma unroll
-        for (int q = p; q >= 1; q /= 2) {
-#pragma unroll
-            for (int j = q % p; j + q < V; j += 2 * q) {
-#pragma unroll
-                for (int i = 0; i < q; ++i) {
-                    if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const uint32_t hi = max(k[i + j], k[i + j + q]);
-                        k[i + j + q] = min(k[i + j], k[i + j + q]);
-                        k[i + j] = hi;
-                    }
-                }
-            }
-        }
-    }
-}
-
+// ------------------------------------------------------------------ packed keys
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -296,191 +315,89 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
-// A float32 score, off by less than score_error(): the exponent's rounding moves exp by
-// |l| 2^-24 (and s (1 - s) |l| by less than 0.3 2^-24), the others are a few ulps.
+// A float32 score, off by less than score_error().
 __device__ __forceinline__ float fast_score(float l, const Args& a, float m, float inv) {
     constexpr float kLog2e = 1.4426950408889634f;
     if (a.sigmoid) return rcp_fast(1.0f + exp2_fast(-l * kLog2e));
     return l == m ? inv : exp2_fast((l - m) * kLog2e) * inv;
 }
 
-// Error bound of a score and of the addition of a bias to it (relative to the choice
-// it gives, where that is larger): 16 ulps of 1, or of the row's largest softmax score inv
-// and 48 more for the rounding of its sum of V + 5 terms.
+// Sigmoid: the exponent's rounding and ex2's two ulps move s by s (1 - s) (|l| 2^-24 +
+// 2^-22) < 0.9 2^-24, the sum and the reciprocal by 1.5 2^-24; bound 6 2^-24.  Softmax: the same
+// and the rounding of its sum of at most 32 + 5 terms a lane, relative to the row's
+// largest score inv; bound 64 2^-24.
 __device__ __forceinline__ float score_error(const Args& a, float inv) {
-    return a.sigmoid ? 1.9073486e-6f : 7.6293945e-6f * inv;
+    return a.sigmoid ? 3.5762787e-7f : 3.8146973e-6f * inv;
 }
-constexpr float kAddError = 2.3841858e-7f;
+constexpr float kRound = 6.0e-8f;  // 2^-24, rounded up
 
-// Which groups stay (bit g).  b1, b2: the two best keys of group `lane`.  `full`: the
-// last group kept and the first dropped cannot be told apart.
-template <int V>
-__device__ __forceinline__ unsigned keep_groups(uint32_t b1, uint32_t b2, const Args& a, float m,
-                                                float inv, int lane, bool& full) {
-    constexpr uint32_t kLow = Packed<V>::kLow;
-    const float lost = a.lost;
-    const bool in = lane < a.n_group;
-    float value = 0.0f, err = 0.0f;
-    if (in && b1 != 0u) {
-        const float c1 = from_key(b1 & ~kLow), c2 = b2 != 0u ? from_key(b2 & ~kLow) : 0.0f;
-        value = c1;
-        err = lost * fabsf(c1);
-        if (a.sums) {
-            if (a.biased) {
-                value = c1 + c2;
-                err += lost * fabsf(c2);
-            } else {  // a score moves by less than its slope times what a logit lost
-                const float s1 = fast_score(c1, a, m, inv);
-                const float s2 = b2 != 0u ? fast_score(c2, a, m, inv) : 0.0f;
-                value = s1 + s2;
-                err = 1.01f * lost * (fabsf(c1) * (a.sigmoid ? s1 * (1.0f - s1) : s1) +
-                                      fabsf(c2) * (a.sigmoid ? s2 * (1.0f - s2) : s2));
-            }
-        }
-        if (a.biased || a.sums)
-            err += 2.0f * score_error(a, inv) + kAddError * (fabsf(c1) + fabsf(c2));
-    }
-    const uint32_t vkey = in && b1 != 0u ? ordered(value) : 0u;
-    int rank = 0;
-    for (int g = 0; g < a.n_group; ++g) {
-        const uint32_t o = __shfl_sync(kAll, vkey, g);
-        rank += o > vkey || (o == vkey && g < lane);
-    }
-    const bool kept = in && rank < a.topk_group;
-    const uint32_t out = __reduce_max_sync(kAll, in && !kept ? vkey : 0u);
-    const uint32_t last = __reduce_min_sync(kAll, kept && vkey != 0u ? vkey : 0xffffffffu);
-    const float worst = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(err)));
-    // bf16 logits without a bias: errors of zero, and equal values go by number
-    if (out != 0u && !(from_key(last) - from_key(out) > 2.0f * worst))
-        full |= a.biased || a.sums || !a.whole_keys;
-    return __ballot_sync(kAll, kept);
+// Keys.  Value part: the low 23 bits of a float in [2^23, 2^24), whose
+// integers they count; everything further than the range below `top`, -inf among it,
+// has value 0.
+constexpr int kNumberBits = 9;
+constexpr uint32_t kNumber = (1u << kNumberBits) - 1u;
+constexpr float kFull = 16777215.0f;   // 2^24 - 1: the value of the largest choice
+constexpr float kNone = 8388608.0f;    // 2^23
+
+__device__ __forceinline__ uint32_t make_key(float c, float top, const Args& a, int number) {
+    if (a.whole_keys) return (ordered(c) & 0xffff0000u) | (kNumber - (uint32_t)number);
+    const float v = fmaxf(fmaf(c - top, a.steps, kFull), kNone);
+    return (__float_as_uint(v) << kNumberBits) | (kNumber - (uint32_t)number);
+}
+// bf16 keys: -inf is below every number's key
+__device__ __forceinline__ bool selectable(uint32_t key, const Args& a) {
+    return key >= (a.whole_keys ? 0x00800000u : 1u << kNumberBits);
+}
+__device__ __forceinline__ int number_of(uint32_t key) { return (int)(kNumber - (key & kNumber)); }
+// The choice, within half a step (exactly for bf16 logits: the bits that a negative
+// one's complement would have set read as zero, so they are set here).
+__device__ __forceinline__ float decode(uint32_t key, float top, const Args& a) {
+    if (a.whole_keys) return from_key((key >> 31) ? key & 0xffff0000u : key | 0x0000ffffu);
+    return top - (kFull - kNone - (float)(key >> kNumberBits)) * (1.0f / a.steps);
 }
 
-// The second attempt.  `mine`: the packed key of candidate `lane` (0: none), k + 1 +
-// kExtra of them in descending order.  False if it does not decide.
-template <int V, typename L>
-__device__ __forceinline__ bool select_candidates(uint32_t mine, const Args& a, const L* row,
-                                                  const float* __restrict__ bias, int lane,
-                                                  int& chosen) {
-    constexpr uint32_t kLow = Packed<V>::kLow;
-    const int n = a.k + 1 + kExtra;
-    const bool live = lane < n && mine != 0u;
-    const int i = live ? (int)(kLow - (mine & kLow)) : 0x7fffffff;
-    double v = -INFINITY;
-    if (live) {
-        v = (double)to_float(__ldg(row + i));
-        if (a.biased) v = sigmoid(v) + (double)__ldg(bias + i);
+// Descending, by Batcher's odd-even merge network.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t* k) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2) {
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q) {
+#pragma unroll
+                for (int i = 0; i < q; ++i) {
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(k[i + j], k[i + j + q]);
+                        k[i + j + q] = min(k[i + j], k[i + j + q]);
+                        k[i + j] = hi;
+                    }
+                }
+            }
+        }
     }
-    int rank = 0;
-    for (int r = 0; r < n; ++r) {
-        const double o = __shfl_sync(kAll, v, r);
-        const int oi = __shfl_sync(kAll, i, r);
-        rank += o > v || (o == v && oi < i);
-    }
-    if (!live) rank = 32;
-    chosen = -1;
-    for (int r = 0; r < n; ++r) {
-        const int of = __shfl_sync(kAll, rank, r);
-        const int oi = __shfl_sync(kAll, i, r);
-        if (of == lane && lane < a.k) chosen = oi;
-    }
-    // every expert that is no candidate lies below the last candidate's key
-    const uint32_t last = __shfl_sync(kAll, mine, n - 1);
-    const unsigned kth = __ballot_sync(kAll, rank == a.k - 1);
-    if (last == 0u || kth == 0u) return true;
-    const float c = from_key(last & ~kLow);
-    const double top = (double)c + (double)(a.lost * fabsf(c)) +
-                       (a.biased ? (double)score_error(a, 1.0f) : 0.0);
-    return __shfl_sync(kAll, v, __ffs(kth) - 1) > top;
 }
 
-// Selects the row's k experts: lane r < k returns the expert of slot r, or -1.  The
-// keys' low bits are the expert's number counted from the top (a lower expert has
-// the larger key).
-template <int V, typename L>
-__device__ __forceinline__ int select(const float (&l)[V], const Args& a, const L* row,
-                                      const float* __restrict__ bias, const float (&bv)[V],
-                                      float m, float sum, int lane) {
-    constexpr int kBits = Packed<V>::kBits;
-    constexpr uint32_t kLow = Packed<V>::kLow;
-    const int i0 = lane * V;
-    const float inv = a.sigmoid ? 1.0f : __fdiv_rn(1.0f, sum);
-    uint32_t key[V];
+// a, b descending: a becomes the KL best of both, descending, `out` the largest of
+// itself and the others.
+template <int KL>
+__device__ __forceinline__ void merge_best(uint32_t (&a)[KL], const uint32_t* b, uint32_t& out) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float c = l[j];
-        if (a.biased && c > -INFINITY) c = fast_score(c, a, m, inv) + bv[j];
-        key[j] = c > -INFINITY ? (ordered(c) & ~kLow) | (kLow - (uint32_t)(i0 + j)) : 0u;
+    for (int i = 0; i < KL; ++i) {  // leaves a bitonic sequence
+        out = max(out, min(a[i], b[KL - 1 - i]));
+        a[i] = max(a[i], b[KL - 1 - i]);
     }
-    bool full = false;
-    if (a.n_group > 1 && !a.group_lanes) {
-        uint32_t b1 = 0u, b2 = 0u;
-        for (int g = 0; g < a.n_group; ++g) {
-            uint32_t t1 = 0u, t2 = 0u;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const unsigned in = (unsigned)(i0 + j - g * a.group_size);
-                merge_top2(t1, t2, in < (unsigned)a.group_size ? key[j] : 0u, 0u);
-            }
-            const uint32_t m1 = __reduce_max_sync(kAll, t1);
-            const uint32_t m2 = __reduce_max_sync(kAll, t1 == m1 ? t2 : t1);
-            if (lane == g) {
-                b1 = m1;
-                b2 = m2;
+    for (int q = KL / 2; q >= 1; q /= 2) {
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+            if ((i & q) == 0) {
+                const uint32_t hi = max(a[i], a[i + q]);
+                a[i + q] = min(a[i], a[i + q]);
+                a[i] = hi;
             }
         }
-        const unsigned keep = keep_groups<V>(b1, b2, a, m, inv, lane, full);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (i0 + j < a.E && !((keep >> ((i0 + j) / a.group_size)) & 1u)) key[j] = 0u;
     }
-    sort_descending(key);
-    if (a.n_group > 1 && a.group_lanes) {
-        uint32_t b1 = key[0], b2 = V > 1 ? key[V > 1 ? 1 : 0] : 0u;
-        for (int off = 1; off < a.group_lanes; off <<= 1) {
-            const uint32_t o1 = __shfl_xor_sync(kAll, b1, off);
-            const uint32_t o2 = __shfl_xor_sync(kAll, b2, off);
-            merge_top2(b1, b2, o1, o2);
-        }
-        const int src = (lane < a.n_group ? lane : 0) * a.group_lanes;
-        b1 = __shfl_sync(kAll, b1, src);
-        b2 = __shfl_sync(kAll, b2, src);
-        const unsigned keep = keep_groups<V>(b1, b2, a, m, inv, lane, full);
-        if (!((keep >> (lane / a.group_lanes)) & 1u)) key[0] = 0u;  // nothing of this lane
-    }
-    uint32_t mine = 0u;
-    auto take = [&](int r) {
-        const uint32_t best = __reduce_max_sync(kAll, key[0]);
-        if (lane == r) mine = best;
-        if (key[0] == best) {
-#pragma unroll
-            for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
-            key[V - 1] = 0u;
-        }
-    };
-    for (int r = 0; r <= a.k; ++r) take(r);
-    bool again = false;
-    const uint32_t next = __shfl_down_sync(kAll, mine, 1);
-    if (lane < a.k && next != 0u) {
-        if (a.biased) {
-            const float hi = from_key(mine & ~kLow), lo = from_key(next & ~kLow);
-            again = !(hi - lo > a.lost * fabsf(lo) + 2.0f * score_error(a, inv) +
-                                    kAddError * (fabsf(hi) + fabsf(lo)));
-        } else {
-            again = !a.whole_keys && (mine >> kBits) == (next >> kBits);
-        }
-    }
-    full = __any_sync(kAll, full);
-    int chosen = lane < a.k && mine != 0u ? (int)(kLow - (mine & kLow)) : -1;
-    if (!full && __any_sync(kAll, again)) {
-        full = true;
-        if (a.sigmoid || !a.biased) {
-            for (int r = a.k + 1; r <= a.k + kExtra; ++r) take(r);
-            full = !select_candidates<V>(mine, a, row, bias, lane, chosen);
-        }
-    }
-    if (full) chosen = select_double<V>(l, a, bias, lane);
-    return chosen;
 }
 
 // Weight of a selected expert before any division by the sum.  With
@@ -493,64 +410,345 @@ __device__ __forceinline__ float sigmoid_ratio(float l, float M) {
     return __fdividef(top, 1.0f + e);
 }
 
-// A warp takes rows t, t + warps, ...; the next row's logits load while it works on one.
+// ------------------------------------------------------------------ forward
+// Place of expert i among the row's LPR * V values.
+template <int V>
+__device__ __forceinline__ int place_of(int i, const Args& a) {
+    if (a.aligned) return i;
+    const int g = i / a.group_size;
+    const int in = i - g * a.group_size;
+    const int part = in / a.lane_size;
+    return (g * a.group_lanes + part) * V + in - part * a.lane_size;
+}
+
+// Copies one row to shared memory in the lanes' order, by the warp.
 template <typename L, int V>
-__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(V))
-    route_kernel(const L* __restrict__ logits, const float* __restrict__ bias,
-                 const uint8_t* __restrict__ mask, const Args a, int32_t* __restrict__ idx,
-                 float* __restrict__ gate) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int i0 = lane * V;
-    const int step = (int)gridDim.x * kWarps;
-    int t = (int)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= a.T) return;
-    float bv[V];
+__device__ __forceinline__ void stage_row(const L* __restrict__ row, const Args& a, int lane,
+                                          L* to) {
+    if (a.aligned) {
+        const int bytes = a.E * (int)sizeof(L);
+        const char* src = reinterpret_cast<const char*>(row);
+        char* dst = reinterpret_cast<char*>(to);
+        if (a.unit == 16) {
+            for (int b = lane * 16; b < bytes; b += 512)
+                *reinterpret_cast<uint4*>(dst + b) = __ldg(reinterpret_cast<const uint4*>(src + b));
+        } else if (a.unit == 8) {
+            for (int b = lane * 8; b < bytes; b += 256)
+                *reinterpret_cast<uint2*>(dst + b) = __ldg(reinterpret_cast<const uint2*>(src + b));
+        } else {
+            for (int i = lane; i < a.E; i += 32) to[i] = __ldg(row + i);
+        }
+    } else {
+        for (int i = lane; i < a.E; i += 32) to[place_of<V>(i, a)] = __ldg(row + i);
+    }
+}
+
+template <int LPR, typename R>
+__device__ __forceinline__ R row_sum(R v) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) bv[j] = a.biased && i0 + j < a.E ? __ldg(bias + i0 + j) : 0.0f;
-    const L* row = logits + (int64_t)t * a.E;
-    const int64_t row_step = (int64_t)step * a.E;
-    int64_t at = (int64_t)t * a.k + lane;
-    RowVec<L, V> ahead;
-    load_row(row, a, i0, ahead);
-    int ahead_mask = mask ? __ldg(mask + t) : 1;
-    while (true) {
-        float l[V];
-        to_floats(ahead, l);
-        const bool routed = ahead_mask != 0, more = t + step < a.T;
-        if (more) {
-            load_row(row + row_step, a, i0, ahead);
-            if (mask) ahead_mask = __ldg(mask + t + step);
+    for (int off = 1; off < LPR; off <<= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
+}
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+    for (int off = 1; off < LPR; off <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+    return v;
+}
+
+// Whether this lane's group stays.  b1, b2: its two best keys.  Each group's value is
+// known to lie in [lo, hi]; `full`: the order of the last kept and first dropped group is
+// not decided by that.
+template <int LPR>
+__device__ __forceinline__ bool keep_group(uint32_t b1, uint32_t b2, const Args& a, float top,
+                                           float m, float inv, float error, int base, int group,
+                                           bool& full) {
+    // a group without a choice: below every other, a lower number first
+    uint32_t lo = (uint32_t)(31 - (group & 31)), hi = lo;
+    if (selectable(b1, a)) {
+        float value, err;
+        const float c1 = decode(b1, top, a);
+        const bool two = selectable(b2, a);
+        const float c2 = two ? decode(b2, top, a) : 0.0f;
+        if (!a.sums) {
+            value = c1;
+            err = error;
+        } else if (a.biased) {
+            value = c1 + c2;
+            err = 2.0f * error + kRound * fabsf(value);
+        } else {  // scores: their own error, and what their logits' error moves them
+            const float s1 = fast_score(c1, a, m, inv), s2 = two ? fast_score(c2, a, m, inv) : 0.0f;
+            value = s1 + s2;
+            err = 2.0f * score_error(a, inv) + 1.01f * error * value;
         }
-        int chosen = -1;
-        float w = 0.0f;
-        if (routed) {
-            float m = 0.0f, sum = 1.0f;
-            if (!a.sigmoid && (a.biased || a.sums || !a.renorm)) softmax_stats<float, V>(l, m, sum);
-            chosen = select<V>(l, a, row, bias, bv, m, sum, lane);
-            const bool taken = chosen >= 0;
-            const float lv = taken ? to_float(__ldg(row + chosen)) : -INFINITY;
-            if (a.renorm) {
-                // the largest selected logit: slot 0's, unless a bias moved it
-                const float M = a.biased ? warp_max_float(lv) : __shfl_sync(kAll, lv, 0);
-                if (taken) w = a.sigmoid ? sigmoid_ratio(lv, M) : exp_below(lv, M);
-                float total = w;  // over the slots, in pairs
-                for (int off = a.slots >> 1; off > 0; off >>= 1)
-                    total += __shfl_xor_sync(kAll, total, off);
-                w = taken ? __fdividef(w, total) : 0.0f;
-            } else if (taken) {
-                w = a.sigmoid ? sigmoid(lv) : __fdividef(exp_below(lv, m), sum);
+        // a second best beyond the range could be anything below it
+        if (a.sums && !two && !a.whole_keys) err = INFINITY;
+        lo = ordered(value - err);
+        hi = ordered(value + err);
+        if (!(err < INFINITY)) {
+            lo = 32u;
+            hi = 0xffffffffu;
+        }
+    } else if (!a.whole_keys && group < a.n_group) {  // dead, or beyond the range
+        hi = ordered(top);
+    }
+    int above = 0, maybe = 0;  // groups surely, and possibly, above this one
+    for (int g = 0; g < a.n_group; ++g) {
+        const uint32_t ol = __shfl_sync(kAll, lo, base + g * a.group_lanes);
+        const uint32_t oh = __shfl_sync(kAll, hi, base + g * a.group_lanes);
+        const bool sure = ol > hi || (lo == hi && ol == oh && ol == lo && g < group);
+        const bool not_below = oh >= lo && !(lo == hi && ol == oh && (ol != lo || g > group));
+        above += sure;
+        maybe += sure || (not_below && g != group);
+    }
+    const bool in = group < a.n_group;
+    full |= in && above < a.topk_group && maybe >= a.topk_group;
+    return in && maybe < a.topk_group;
+}
+
+// The choice of a biased expert; a NaN (an unset place's bias, a NaN bias) reads -inf.
+__device__ __forceinline__ float biased_choice(float l, float b, const Args& a, float m,
+                                               float inv) {
+    const float c = fmaxf(fast_score(l, a, m, inv) + b, -INFINITY);
+    return l > -INFINITY ? c : -INFINITY;
+}
+
+// Rows in work per warp: 32 / LPR, next to each other.
+template <typename L, int LPR, int V, int KL>
+__global__ void __launch_bounds__(kForwardWarps * 32)
+    route_kernel(const L* __restrict__ logits, const float* __restrict__ bias,
+                 const uint8_t* __restrict__ mask, const __grid_constant__ Args a,
+                 int32_t* __restrict__ idx, float* __restrict__ gate) {
+    constexpr int kRows = 32 / LPR;
+    constexpr int kPitch = LPR * V + 16 / (int)sizeof(L);  // rows start 4 banks apart
+    __shared__ __align__(16) L s_rows[kForwardWarps][kRows * kPitch];
+    __shared__ double s_choice[kForwardWarps][LPR * V < kScoredMaxE ? LPR * V : kScoredMaxE];
+    __shared__ __align__(16) float s_bias[LPR * V];  // in the lanes' order
+    grid_dependency_wait();
+    if (a.biased) {
+        for (int i = threadIdx.x; i < a.E; i += kForwardWarps * 32)
+            s_bias[place_of<V>(i, a)] = __ldg(bias + i);
+        __syncthreads();
+    }
+    const int lane = threadIdx.x & 31;
+    const int sub = lane & (LPR - 1), base = lane - sub;  // lane of the row, its first lane
+    L* rows = s_rows[threadIdx.x >> 5];
+    const int t0 = ((int)blockIdx.x * kForwardWarps + (threadIdx.x >> 5)) * kRows;
+    if (t0 >= a.T) return;
+    const int t = t0 + lane / LPR;
+    const bool routed = t < a.T && (!mask || __ldg(mask + t) != 0);
+
+    // the lanes' values that no expert fills read -inf
+    const int group = sub / a.group_lanes, part = sub - group * a.group_lanes;
+    const int first = group * a.group_size + part * a.lane_size;
+    const int count = group < a.n_group
+                          ? max(0, min(a.lane_size, a.group_size - part * a.lane_size))
+                          : 0;
+    L* mine = rows + (lane / LPR) * kPitch + sub * V;
+    if (count < V) {
+        for (int j = count; j < V; ++j) mine[j] = (L)(-INFINITY);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (t0 + r < a.T)
+            stage_row<L, V>(logits + (int64_t)(t0 + r) * a.E, a, lane, rows + r * kPitch);
+    __syncwarp();
+
+    // this lane's logits, 16 bytes at a time from a place that turns with the lane, so
+    // that the lanes' reads lie in different banks; value j is expert at(j)
+    constexpr int kPer = 16 / (int)sizeof(L);  // values of a piece
+    constexpr int kPieces = V / kPer > 0 ? V / kPer : 1;
+    float l[V];
+    const int turn = (sub * V / (kPer * 8)) & (kPieces - 1);
+    auto at = [&](int j) {
+        return V <= kPer ? first + j
+                         : first + (((j / kPer + turn) & (kPieces - 1)) * kPer) + j % kPer;
+    };
+    if constexpr (V >= kPer) {
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+            union {
+                uint4 u;
+                L v[kPer];
+            } q;
+            q.u = *reinterpret_cast<const uint4*>(mine + ((c + turn) & (kPieces - 1)) * kPer);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) l[c * kPer + j] = fmaxf(to_float(q.v[j]), -INFINITY);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] = fmaxf(to_float(mine[j]), -INFINITY);
+    }
+
+    float m = 0.0f, sum = 1.0f;
+    if (!a.sigmoid && (a.biased || a.sums || !a.renorm)) {
+        m = l[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
+        m = row_max<LPR>(m);
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += l[j] > -INFINITY ? fast_score(l[j], a, m, 1.0f) : 0.0f;
+        sum = row_sum<LPR>(sum);
+    }
+    const float inv = a.sigmoid ? 1.0f : __fdividef(1.0f, sum);
+
+    if (a.biased) {
+        const float* b = s_bias + sub * V - first;
+        if constexpr (V >= 4) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(b + at(j));
+                l[j] = biased_choice(l[j], q.x, a, m, inv);
+                l[j + 1] = biased_choice(l[j + 1], q.y, a, m, inv);
+                l[j + 2] = biased_choice(l[j + 2], q.z, a, m, inv);
+                l[j + 3] = biased_choice(l[j + 3], q.w, a, m, inv);
             }
-            w *= a.scale;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[j] = biased_choice(l[j], b[at(j)], a, m, inv);
         }
-        if (lane < a.k) {
-            idx[at] = chosen;
-            gate[at] = w;
+    }
+    float top = 0.0f;  // the row's largest choice
+    if (!a.whole_keys) {
+        top = l[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) top = fmaxf(top, l[j]);
+        top = row_max<LPR>(top);
+    }
+    uint32_t key[V > KL ? V : KL];
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = make_key(l[j], top, a, at(j));
+    // error of a choice as a key of distance `d` from the top tells it: half a step, the
+    // roundings of the distance and of score + bias, and the score's error
+    const float step = 1.0f / a.steps;
+    auto key_error = [&](float d) {
+        if (a.whole_keys) return 0.0f;
+        return 0.5f * step + kRound * d +
+               (a.biased ? score_error(a, inv) + kRound * (fabsf(top) + d) : 0.0f);
+    };
+    uint32_t best[KL], out = 0u;
+    constexpr int kFirst = V < KL ? V : KL;
+    sort_descending<kFirst>(key);
+#pragma unroll
+    for (int j = 0; j < KL; ++j) best[j] = j < kFirst ? key[j] : 0u;
+#pragma unroll
+    for (int b = KL; b < V; b += KL) {
+        sort_descending<KL>(key + b);
+        merge_best<KL>(best, key + b, out);
+    }
+    bool full = false;
+    if (a.n_group > 1) {
+        uint32_t b1 = best[0], b2 = best[1];
+        for (int off = 1; off < a.group_lanes; off <<= 1) {
+            const uint32_t o1 = __shfl_xor_sync(kAll, b1, off);
+            const uint32_t o2 = __shfl_xor_sync(kAll, b2, off);
+            merge_top2(b1, b2, o1, o2);
         }
-        if (!more) return;
-        t += step;
-        row += row_step;
-        at += (int64_t)step * a.k;
+        if (!keep_group<LPR>(b1, b2, a, top, m, inv, key_error(8388608.0f * step), base, group,
+                             full)) {
+#pragma unroll
+            for (int j = 0; j < KL; ++j) best[j] = 0u;
+            out = 0u;
+        }
+    }
+#pragma unroll
+    for (int off = 1; off < LPR; off <<= 1) {
+        uint32_t other[KL];
+#pragma unroll
+        for (int j = 0; j < KL; ++j) other[j] = __shfl_xor_sync(kAll, best[j], off);
+        out = max(out, __shfl_xor_sync(kAll, out, off));
+        merge_best<KL>(best, other, out);
+    }
+    // slot `sub` of the row and the key behind it
+    uint32_t slot = 0u, next = 0u;
+#pragma unroll
+    for (int j = 0; j < KL; ++j)
+        if (sub == j) {
+            slot = best[j];
+            next = j + 1 < KL ? best[j + 1 < KL ? j + 1 : j] : out;
+        }
+    bool again = false;
+    // values that may be the other way round: logits' keys keep the order, biased ones are off
+    const float far = (float)(0x7fffffu - (next >> kNumberBits)) * step;
+    const uint32_t apart = a.biased ? (uint32_t)(2.0f * key_error(far) * a.steps) + 1u : 0u;
+    if (sub < a.k) {
+        if (a.whole_keys) {
+            // exact: equal logits go by number
+        } else if (!selectable(slot, a)) {
+            full = true;  // dead, or beyond the range
+        } else {
+            again = (slot >> kNumberBits) - (next >> kNumberBits) <= apart;
+        }
+    }
+    int chosen = sub < a.k && selectable(slot, a) ? number_of(slot) : -1;
+
+    if (__any_sync(kAll, (full || again) && routed)) {
+        unsigned fulls = __ballot_sync(kAll, full && routed);
+        if (a.sigmoid || !a.biased) {
+            // second attempt, for all rows of the warp alike
+            const bool live = selectable(slot, a);
+            const int i = live ? number_of(slot) : 0x7fffffff;
+            double v = -INFINITY;
+            if (live) {
+                v = (double)to_float(rows[(lane / LPR) * kPitch + place_of<V>(i, a)]);
+                if (a.biased) v = score_double(v, true, 0.0, 1.0) + (double)__ldg(bias + i);
+            }
+            int rank = 0;
+#pragma unroll
+            for (int r = 0; r < KL; ++r) {
+                const double o = __shfl_sync(kAll, v, base + r);
+                const int oi = __shfl_sync(kAll, i, base + r);
+                rank += o > v || (o == v && oi < i);
+            }
+            if (!live) rank = 64;
+            int ranked = -1;
+#pragma unroll
+            for (int r = 0; r < KL; ++r) {
+                const int of = __shfl_sync(kAll, rank, base + r);
+                const int oi = __shfl_sync(kAll, i, base + r);
+                if (of == sub && sub < a.k) ranked = oi;
+            }
+            chosen = ranked;
+            // `out` may be as high as the k-th, and more with it
+            const float out_far = (float)(0x7fffffu - (out >> kNumberBits)) * step;
+            const uint32_t out_apart =
+                a.biased ? (uint32_t)(2.0f * key_error(out_far) * a.steps) + 1u : 0u;
+            fulls |= __ballot_sync(kAll, routed && !a.whole_keys && rank == a.k - 1 &&
+                                             (slot >> kNumberBits) - (out >> kNumberBits) <=
+                                                 out_apart);
+        } else {
+            fulls |= __ballot_sync(kAll, again && routed);
+        }
+        for (int r = 0; r < kRows; ++r) {  // third attempt, row by row
+            const unsigned of_row = LPR == 32 ? kAll : ((1u << (LPR & 31)) - 1u) << (r * LPR);
+            if (!(fulls & of_row)) continue;
+            const int got = select_double<L>(logits + (int64_t)(t0 + r) * a.E, a, bias, lane,
+                                            s_choice[threadIdx.x >> 5]);
+            const int to = __shfl_sync(kAll, got, sub);
+            if (lane / LPR == r) chosen = sub < a.k ? to : -1;
+        }
+    }
+
+    float w = 0.0f;
+    if (!routed) chosen = -1;
+    const bool taken = chosen >= 0;
+    const float lv =
+        taken ? to_float(rows[(lane / LPR) * kPitch + place_of<V>(chosen, a)]) : -INFINITY;
+    if (a.renorm) {
+        // the largest selected logit: slot 0's, unless a bias moved it
+        const float M = a.biased ? row_max<LPR>(lv) : __shfl_sync(kAll, lv, base);
+        if (taken) w = a.sigmoid ? sigmoid_ratio(lv, M) : exp_below(lv, M);
+        float total = w;  // over the slots, in pairs
+        for (int off = a.slots >> 1; off > 0; off >>= 1)
+            total += __shfl_xor_sync(kAll, total, off);
+        w = taken ? __fdividef(w, total) : 0.0f;
+    } else if (taken) {
+        w = a.sigmoid ? sigmoid(lv) : __fdividef(exp_below(lv, m), sum);
+    }
+    if (t < a.T && sub < a.k) {
+        idx[(int64_t)t * a.k + sub] = chosen;
+        gate[(int64_t)t * a.k + sub] = w * a.scale;
     }
 }
 
@@ -676,7 +874,15 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(V))
 }
 
 // ------------------------------------------------------------------ host side
-Args make_args(const moe_shape& s, const moe_scoring& r, bool has_bias, int V, int esize) {
+int pow2_ceil(int n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+int unit_of(int bytes) { return bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : bytes % 4 == 0 ? 4 : 2; }
+
+Args make_args(const moe_shape& s, const moe_scoring& r, bool has_bias, int esize) {
     Args a{};
     a.T = s.T;
     a.E = s.E;
@@ -687,19 +893,70 @@ Args make_args(const moe_shape& s, const moe_scoring& r, bool has_bias, int V, i
     a.group_size = s.E / r.n_group;
     a.topk_group = r.topk_group;
     a.group_top = r.group_top;
-    const int lanes = a.group_size % V == 0 ? a.group_size / V : 0;
-    a.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
     a.biased = has_bias;
     a.sums = r.n_group > 1 && r.group_top > 1;
     a.whole_keys = esize == 2 && !has_bias;
-    // V experts a lane: 2^B >= 32 V numbers in the low bits of 23
-    a.lost = a.whole_keys ? 0.0f : std::ldexp(1.01f, (V == 1 ? 5 : V == 2 ? 6 : V == 4 ? 7 : V == 8 ? 8 : 9) - 23);
-    const int unit = V * esize < 16 ? V * esize : 16;
-    a.vec = (s.E * esize) % unit == 0;
+    a.steps = 8388608.0f / (has_bias ? 4.0f : 32.0f);
+    a.slots = pow2_ceil(s.k);
+    a.unit = unit_of(s.E * esize);
     a.scale = r.scale;
-    a.slots = 1;
-    while (a.slots < s.k) a.slots *= 2;
     return a;
+}
+
+// Lanes to a row and values to a lane: as few lanes as hold the slots, a power of two of
+// them for each group and no more than 32 values.
+struct Fit {
+    int lanes, values;
+};
+Fit fit(const moe_shape& s, Args& a) {
+    const int groups = pow2_ceil(a.n_group);
+    // a batch that leaves schedulers idle: a warp a row, which is the shortest chain
+    const int64_t warps = (int64_t)device_sm_count() * 4;
+    int lanes = std::max(s.T <= warps && s.E > 32 ? 32 : s.k <= 8 ? 8 : 16, groups);
+    int per = 0, values = 0;
+    for (;; lanes *= 2) {
+        a.group_lanes = lanes / groups;
+        per = (a.group_size + a.group_lanes - 1) / a.group_lanes;
+        values = per <= 1 && lanes == 8 ? 1 : per <= 4 ? 4 : per <= 8 && lanes == 8 ? 8
+                 : per <= 16 ? 16 : 32;
+        if (per <= 32 || lanes == 32) break;
+    }
+    // one group: lanes filled to the last; several: their experts spread evenly
+    a.lane_size = a.n_group == 1 ? values : per;
+    a.aligned = a.n_group == 1 || (per == values && a.group_size == values * a.group_lanes);
+    return Fit{lanes, values};
+}
+
+template <typename L, int LPR, int V, int KL>
+int launch_route(const moe_shape& s, const Args& a, const void* logits, const float* bias,
+                 const uint8_t* mask, int32_t* idx, float* gate, cudaStream_t st) {
+    constexpr int kRows = kForwardWarps * 32 / LPR;
+    return launch_pdl(route_kernel<L, LPR, V, KL>, dim3((s.T + kRows - 1) / kRows),
+                      dim3(kForwardWarps * 32), 0, st, static_cast<const L*>(logits), bias, mask, a,
+                      idx, gate) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+template <typename L, int KL, typename... Rest>
+int route_lanes(const Fit& f, Rest... rest) {
+    if constexpr (KL == 8) {
+        if (f.lanes == 8) {
+            if (f.values == 1) return launch_route<L, 8, 1, KL>(rest...);
+            if (f.values == 4) return launch_route<L, 8, 4, KL>(rest...);
+            if (f.values == 8) return launch_route<L, 8, 8, KL>(rest...);
+            if (f.values == 16) return launch_route<L, 8, 16, KL>(rest...);
+            return launch_route<L, 8, 32, KL>(rest...);
+        }
+    }
+    if (f.lanes == 16) {
+        if (f.values == 4) return launch_route<L, 16, 4, KL>(rest...);
+        if (f.values == 16) return launch_route<L, 16, 16, KL>(rest...);
+        return launch_route<L, 16, 32, KL>(rest...);
+    }
+    if (f.values == 4) return launch_route<L, 32, 4, KL>(rest...);
+    if (f.values == 16) return launch_route<L, 32, 16, KL>(rest...);
+    return launch_route<L, 32, 32, KL>(rest...);
 }
 
 // Blocks of kWarps rows each, no more than fit at once (the warps then loop).
@@ -709,19 +966,10 @@ unsigned blocks_for(int T, int V) {
 }
 
 template <typename L, int V>
-int launch_route(const moe_shape& s, const moe_scoring& r, const void* logits, const float* bias,
-                 const uint8_t* mask, int32_t* idx, float* gate, cudaStream_t st) {
-    const Args a = make_args(s, r, bias != nullptr, V, sizeof(L));
-    return launch_pdl(route_kernel<L, V>, dim3(blocks_for(s.T, V)), dim3(kWarps * 32), 0,
-                      st, static_cast<const L*>(logits), bias, mask, a, idx, gate) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
-}
-
-template <typename L, int V>
 int launch_backward(const moe_shape& s, const moe_scoring& r, const void* logits,
                     const int32_t* idx, const float* dgate, void* dlogits, cudaStream_t st) {
-    const Args a = make_args(s, r, false, V, sizeof(L));
+    Args a = make_args(s, r, false, sizeof(L));
+    a.vec = a.unit >= std::min(16, V * (int)sizeof(L));
     return launch_pdl(backward_kernel<L, V>, dim3(blocks_for(s.T, V)), dim3(kWarps * 32),
                       0, st, static_cast<const L*>(logits), idx, dgate, a,
                       static_cast<L*>(dlogits)) == cudaSuccess
@@ -729,13 +977,13 @@ int launch_backward(const moe_shape& s, const moe_scoring& r, const void* logits
                : MOE_ERR_CUDA;
 }
 
-template <typename L, typename... Rest>
-int route_for(const moe_shape& s, Rest... rest) {
-    if (s.E <= 32) return launch_route<L, 1>(s, rest...);
-    if (s.E <= 64) return launch_route<L, 2>(s, rest...);
-    if (s.E <= 128) return launch_route<L, 4>(s, rest...);
-    if (s.E <= 256) return launch_route<L, 8>(s, rest...);
-    return launch_route<L, 16>(s, rest...);
+template <typename L>
+int route_for(const moe_shape& s, const moe_scoring& r, const void* logits, const float* bias,
+              const uint8_t* mask, int32_t* idx, float* gate, cudaStream_t st) {
+    Args a = make_args(s, r, bias != nullptr, sizeof(L));
+    const Fit f = fit(s, a);
+    return s.k <= 8 ? route_lanes<L, 8>(f, s, a, logits, bias, mask, idx, gate, st)
+                    : route_lanes<L, 16>(f, s, a, logits, bias, mask, idx, gate, st);
 }
 
 template <typename L, typename... Rest>

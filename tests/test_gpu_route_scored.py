@@ -19,6 +19,10 @@ def _logits(T, E, seed, dtype=torch.float32):
     return (2.0 * torch.randn(T, E, generator=gen, device="cuda")).to(dtype)
 
 
+def _gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
 def _run(l, k, sc, bias=None, mask=None):
     T, E = l.shape
     return moe.moe_route_scored((T, 128, 128, E, k), l, moe.MoeScoring(**sc), bias=bias, mask=mask)
@@ -58,6 +62,13 @@ CASES = [
     (300, 10, dict(score="softmax", n_group=5, topk_group=5, group_top=2)),
     (512, 16, dict(score="sigmoid", n_group=16, topk_group=2, group_top=2)),
     (512, 8, dict(score="softmax", renorm=False)),
+    (16, 2, dict(score="sigmoid", n_group=16, topk_group=7)),
+    (48, 3, dict(score="softmax", n_group=3, topk_group=1, group_top=2)),
+    (504, 8, dict(score="sigmoid", n_group=9, topk_group=4, group_top=2)),
+    (510, 12, dict(score="softmax", n_group=17, topk_group=8, group_top=2)),
+    (500, 7, dict(score="sigmoid", n_group=2, topk_group=1)),
+    (62, 2, dict(score="sigmoid", n_group=31, topk_group=9, group_top=2)),
+    (256, 13, dict(score="softmax", n_group=8, topk_group=4)),
 ]
 
 
@@ -143,6 +154,20 @@ def test_choices_closer_than_float32_resolves(E, groups):
     sc["score"] = "softmax"
     bias = (1.0 - torch.softmax(l[0].double(), 0)).float()
     _check(l, 8, sc, bias)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-43, 1e-3, 30.0, 1e4])
+@pytest.mark.parametrize("tops", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_of_every_size(score, tops, scale, dtype):
+    """Mostly negative logits, subnormal to huge, with groups valued by their logits or by
+    sums of scores; a biased selection on the same."""
+    E, groups = 128, 16
+    l = ((torch.randn(60, E, generator=_gen(3), device="cuda") - 1.5) * scale).to(dtype)
+    sc = dict(score=score, n_group=groups, topk_group=5, group_top=tops)
+    _check(l, 6, sc)
+    _check(l, 6, sc, torch.linspace(-0.3, 0.3, E, device="cuda"))
 
 
 def test_equal_choices_go_to_the_lower_index():
