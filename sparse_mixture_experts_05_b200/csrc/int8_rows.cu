@@ -157,13 +157,14 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// A warp a row up to 2048 values, when there are rows for it: less than 8 warps of a
-// block would have work, or wait for the others (32792 rows of 768: 20 us by blocks).
+// A warp a row up to 1536 values, when there are rows for it: less than 8 warps of a
+// block would have work, or wait for the others (32792 rows of 768: 14 us by warps, 20
+// by blocks; 4099 rows of 2048 to 8 places each: 14 and 12).
 template <bool kScatter>
 int launch_quantize(const void* x, int64_t rows, int cols, const int32_t* map, int k, int8_t* xq,
                     float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t st) {
     const int units = cols / 16;
-    const bool by_warp = units <= 128 && rows >= 1024;
+    const bool by_warp = units <= 96 && rows >= 1024;
     const int threads = by_warp ? 256 : std::min(256, (units + 31) / 32 * 32);
     const int per = by_warp ? (units + 31) / 32 : (units + threads - 1) / threads;
     const int64_t blocks = by_warp ? (rows + 7) / 8 : rows;
@@ -286,8 +287,20 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
     return r;
 }
 
+// Lanes of the warp with this lane's expert e (of E <= 2^bits), none for e < 0: one ballot
+// for each bit of the number.  (The match instruction takes longer the more numbers it
+// finds; with 128 experts it made the kernel 16 us for 32792 slots.)
+__device__ __forceinline__ unsigned lanes_with(int e, int bits) {
+    unsigned same = __ballot_sync(kAll, e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const unsigned set = __ballot_sync(kAll, (e >> b) & 1);
+        same &= ((e >> b) & 1) ? set : ~set;
+    }
+    return e >= 0 ? same : 0u;
+}
+
 __global__ void __launch_bounds__(kIndexThreads, 1)
-    index_many_kernel(const int32_t* __restrict__ idx, int n, int E, int k,
+    index_many_kernel(const int32_t* __restrict__ idx, int n, int E, int bits, int k,
                       int32_t* __restrict__ offsets, int32_t* __restrict__ perm_tok,
                       int32_t* __restrict__ inv) {
     extern __shared__ int s_pos[];  // [32][E + 1]: counts, then positions within the CTA
@@ -319,7 +332,7 @@ __global__ void __launch_bounds__(kIndexThreads, 1)
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (base + u * 32 >= j1) break;
-            const unsigned same = __match_any_sync(kAll, ids[u]);
+            const unsigned same = lanes_with(ids[u], bits);
             if (ids[u] >= 0 && (same & lt) == 0) pos[ids[u]] += __popc(same);
             __syncwarp();
         }
@@ -378,7 +391,7 @@ __global__ void __launch_bounds__(kIndexThreads, 1)
             if (base + u * 32 >= j1) break;
             const int j = base + u * 32 + lane;
             const int e = ids[u];
-            const unsigned same = __match_any_sync(kAll, e);
+            const unsigned same = lanes_with(e, bits);
             int p = -1;
             if (e >= 0) {
                 p = pos[e] + s_base[e] + __popc(same & lt);
@@ -447,6 +460,8 @@ int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* 
     int C = 1;
     while (C < kMaxCluster && n > (int64_t)C * kIndexWarps * kSlotsPerWarp) C *= 2;
     const int smem = kIndexWarps * (s.E + 1) * 4;
+    int bits = 0;
+    while ((1 << bits) < s.E) ++bits;
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(index_many_kernel),
                              kIndexWarps * (kMaxE + 1) * 4))
         return MOE_ERR_CUDA;
@@ -464,7 +479,7 @@ int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, (int)n, (int)s.E, (int)s.k, offsets,
+    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, (int)n, (int)s.E, bits, (int)s.k, offsets,
                               perm_tok, inv) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;

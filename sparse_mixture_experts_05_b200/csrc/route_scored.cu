@@ -421,24 +421,37 @@ __device__ __forceinline__ int place_of(int i, const Args& a) {
     return (g * a.group_lanes + part) * V + in - part * a.lane_size;
 }
 
-// Copies one row to shared memory in the lanes' order, by the warp.
+// One asynchronous copy to shared memory.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(from), "n"(kBytes)
+                 : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void stage_bytes(const void* row, int bytes, int lane, void* to) {
+    for (int b = lane * kBytes; b < bytes; b += 32 * kBytes)
+        copy_async<kBytes>(static_cast<char*>(to) + b, static_cast<const char*>(row) + b);
+}
+
+// Copies one row to shared memory in the lanes' order, by the warp.  Asynchronously where
+// the copy unit has the size for it, so that a warp's rows are all on their way at once
+// (one after the other they cost 0.3 us each).
 template <typename L, int V>
 __device__ __forceinline__ void stage_row(const L* __restrict__ row, const Args& a, int lane,
                                           L* to) {
-    if (a.aligned) {
-        const int bytes = a.E * (int)sizeof(L);
-        const char* src = reinterpret_cast<const char*>(row);
-        char* dst = reinterpret_cast<char*>(to);
-        if (a.unit == 16) {
-            for (int b = lane * 16; b < bytes; b += 512)
-                *reinterpret_cast<uint4*>(dst + b) = __ldg(reinterpret_cast<const uint4*>(src + b));
-        } else if (a.unit == 8) {
-            for (int b = lane * 8; b < bytes; b += 256)
-                *reinterpret_cast<uint2*>(dst + b) = __ldg(reinterpret_cast<const uint2*>(src + b));
-        } else {
-            for (int i = lane; i < a.E; i += 32) to[i] = __ldg(row + i);
-        }
+    const int bytes = a.E * (int)sizeof(L);
+    if (a.aligned && a.unit == 16) {
+        stage_bytes<16>(row, bytes, lane, to);
+    } else if (a.aligned && a.unit == 8) {
+        stage_bytes<8>(row, bytes, lane, to);
+    } else if (a.aligned && a.unit == 4) {
+        stage_bytes<4>(row, bytes, lane, to);
+    } else if constexpr (sizeof(L) == 4) {
+        for (int i = lane; i < a.E; i += 32) copy_async<4>(to + place_of<V>(i, a), row + i);
     } else {
+#pragma unroll 4
         for (int i = lane; i < a.E; i += 32) to[place_of<V>(i, a)] = __ldg(row + i);
     }
 }
@@ -552,6 +565,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
     for (int r = 0; r < kRows; ++r)
         if (t0 + r < a.T)
             stage_row<L, V>(logits + (int64_t)(t0 + r) * a.E, a, lane, rows + r * kPitch);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
 
     // this lane's logits, 16 bytes at a time from a place that turns with the lane, so
@@ -940,7 +954,7 @@ int launch_route(const moe_shape& s, const Args& a, const void* logits, const fl
 
 template <typename L, int KL, typename... Rest>
 int route_lanes(const Fit& f, Rest... rest) {
-    if constexpr (KL == 8) {
+    if constexpr (KL <= 8) {
         if (f.lanes == 8) {
             if (f.values == 1) return launch_route<L, 8, 1, KL>(rest...);
             if (f.values == 4) return launch_route<L, 8, 4, KL>(rest...);
@@ -982,8 +996,9 @@ int route_for(const moe_shape& s, const moe_scoring& r, const void* logits, cons
               const uint8_t* mask, int32_t* idx, float* gate, cudaStream_t st) {
     Args a = make_args(s, r, bias != nullptr, sizeof(L));
     const Fit f = fit(s, a);
-    return s.k <= 8 ? route_lanes<L, 8>(f, s, a, logits, bias, mask, idx, gate, st)
-                    : route_lanes<L, 16>(f, s, a, logits, bias, mask, idx, gate, st);
+    if (s.k <= 2) return route_lanes<L, 2>(f, s, a, logits, bias, mask, idx, gate, st);
+    if (s.k <= 8) return route_lanes<L, 8>(f, s, a, logits, bias, mask, idx, gate, st);
+    return route_lanes<L, 16>(f, s, a, logits, bias, mask, idx, gate, st);
 }
 
 template <typename L, typename... Rest>
