@@ -149,16 +149,14 @@ int moe_quantize_weights_int8(int E, int K, int N, const void* W, int8_t* Wq, fl
 
 int moe_dispatch_int8(moe_shape s, const int32_t* idx, const void* x, int32_t* offsets,
                       int32_t* perm_tok, int32_t* inv, int8_t* xq, float* xs, void* stream) {
-    int rc = check_shape(s);
+    const int rc = check_shape(s);
     if (rc) return rc;
     if (!ok_ptr(offsets)) return MOE_ERR_INVALID_ARG;
     if (s.T > 0 && (!ok_ptr(idx) || !ok_ptr(x) || !ok_ptr(perm_tok) || !ok_ptr(inv) ||
                     !ok_ptr(xq) || !ok_ptr(xs)))
         return MOE_ERR_INVALID_ARG;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    rc = launch_dispatch_index_many(s, idx, offsets, perm_tok, inv, st);
-    if (rc || s.T == 0) return rc;
-    return launch_quantize_scatter(s, x, inv, xq, xs, nullptr, 0, st);
+    return launch_dispatch_quantize(s, idx, x, offsets, perm_tok, inv, xq, xs, nullptr, 0,
+                                    static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_expert_swiglu_int8_workspace_bytes(moe_shape s) {
@@ -224,11 +222,10 @@ int moe_forward_int8(moe_shape s, const void* x, const void* logits, int logits_
     rc = launch_route_scored(s, r, logits, logits_type == MOE_LOGITS_BF16, route_bias, mask, idx,
                              gate, st);
     if (rc) return rc;
-    rc = launch_dispatch_index_many(s, idx, offsets, at<int32_t>(ws, L.perm), inv, st);
-    if (rc) return rc;
     // the row kernel also clears the status word and the tile counters
-    rc = launch_quantize_scatter(s, x, inv, xq, xs, static_cast<uint32_t*>(ws),
-                                 (int64_t)(int8_workspace(s).zero_bytes / 4), st);
+    rc = launch_dispatch_quantize(s, idx, x, offsets, at<int32_t>(ws, L.perm), inv, xq, xs,
+                                  static_cast<uint32_t*>(ws),
+                                  (int64_t)(int8_workspace(s).zero_bytes / 4), st);
     if (rc) return rc;
     rc = expert_products_int8(s, xq, xs, offsets, Int8Experts{W1q, s1, W3q, s3, W2q, s2}, o, ws,
                               static_cast<int*>(ws), kDefaultWaitTimeoutNs, -1, st);

@@ -95,11 +95,56 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* s_max) {
     return all;
 }
 
-// A block, or (kWarpRow) a warp, quantises one row of `units` x 16 values; NU > 0:
-// the row stays in registers (NU units a thread), 0: it is read twice (the second time
-// from L2).  kScatter: row t goes to its k sorted rows; otherwise row r to row r
-// itself, if r < *map.  Both directions are whole vectors of consecutive bytes, so the
-// memory bounds them: rows of 14336 values, 8192 of them, 54 us (6.5 TB/s).
+// Reads the row at `src` (`units` x 16 values, `threads` of them a row's) and returns
+// its multiplier.  NU > 0: the row stays in v (NU units a thread); 0: it is read again
+// when it is written.
+template <int NU, bool kWarpRow>
+__device__ __forceinline__ Quant read_row(const uint4* __restrict__ src, int units, int tid,
+                                          int threads, uint4 (&v)[NU > 0 ? NU : 1][2],
+                                          uint32_t* s_max) {
+    uint32_t m = 0;
+    if constexpr (NU > 0) {
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            const int u = tid + n * threads;
+            v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (u < units) {
+                v[n][0] = __ldg(src + 2 * u);
+                v[n][1] = __ldg(src + 2 * u + 1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NU; ++n) m = max_abs16(v[n][0], v[n][1], m);
+    } else {
+        for (int u = tid; u < units; u += threads)
+            m = max_abs16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), m);
+    }
+    return make_quant(row_max<kWarpRow>(m, s_max));
+}
+
+// Writes the row read by read_row to row dst.
+template <int NU>
+__device__ __forceinline__ void write_row(const uint4* __restrict__ src, int units, int tid,
+                                          int threads, const uint4 (&v)[NU > 0 ? NU : 1][2],
+                                          const Quant& q, int64_t dst, uint4* __restrict__ xq,
+                                          float* __restrict__ xs) {
+    if (tid == 0) xs[dst] = q.scale;
+    if constexpr (NU > 0) {
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            const int u = tid + n * threads;
+            if (u < units) xq[dst * units + u] = quantize16(v[n][0], v[n][1], q);
+        }
+    } else {
+        for (int u = tid; u < units; u += threads)
+            xq[dst * units + u] = quantize16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), q);
+    }
+}
+
+// A block, or (kWarpRow) a warp, quantises one row.  kScatter: row t goes to its k
+// sorted rows; otherwise row r to row r itself, if r < *map.  Both directions are whole
+// vectors of consecutive bytes, so the memory bounds them: rows of 14336 values, 8192 of
+// them, 54 us (6.5 TB/s).
 template <int NU, bool kScatter, bool kWarpRow>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const uint4* __restrict__ x, int64_t rows, int units,
@@ -121,40 +166,69 @@ __global__ void __launch_bounds__(256)
     }
     const uint4* src = x + row * units * 2;
     uint4 v[NU > 0 ? NU : 1][2];
-    uint32_t m = 0;
-    if constexpr (NU > 0) {
-#pragma unroll
-        for (int n = 0; n < NU; ++n) {
-            const int u = tid + n * threads;
-            v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (u < units) {
-                v[n][0] = __ldg(src + 2 * u);
-                v[n][1] = __ldg(src + 2 * u + 1);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NU; ++n) m = max_abs16(v[n][0], v[n][1], m);
-    } else {
-        for (int u = tid; u < units; u += threads)
-            m = max_abs16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), m);
-    }
-    const Quant q = make_quant(row_max<kWarpRow>(m, s_max));
+    const Quant q = read_row<NU, kWarpRow>(src, units, tid, threads, v, s_max);
     const int copies = kScatter ? k : 1;
     for (int s = 0; s < copies; ++s) {
         const int64_t dst = kScatter ? (int64_t)__ldg(map + row * k + s) : row;
-        if (dst < 0) continue;
-        if (tid == 0) xs[dst] = q.scale;
-        if constexpr (NU > 0) {
-#pragma unroll
-            for (int n = 0; n < NU; ++n) {
-                const int u = tid + n * threads;
-                if (u < units) xq[dst * units + u] = quantize16(v[n][0], v[n][1], q);
-            }
-        } else {
-            for (int u = tid; u < units; u += threads)
-                xq[dst * units + u] = quantize16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1), q);
+        if (dst >= 0) write_row<NU>(src, units, tid, threads, v, q, dst, xq, xs);
+    }
+}
+
+// Token lists and quantised rows of a small batch (T * k <= kSmallSlots) in one launch:
+// block t counts, over all slots, where its token's k rows go (slots of a lower
+// expert, and earlier slots of the same one), and the blocks share the offsets.  The
+// same lists as the index kernels give, without the 4 us of their launch.
+constexpr int kSmallSlots = 1024;
+constexpr int kSmallThreads = 256;
+
+template <int NU>
+__global__ void __launch_bounds__(kSmallThreads)
+    small_dispatch_kernel(const int32_t* __restrict__ idx, const uint4* __restrict__ x, int T,
+                          int E, int k, int units, int32_t* __restrict__ offsets,
+                          int32_t* __restrict__ perm_tok, int32_t* __restrict__ inv,
+                          uint4* __restrict__ xq, float* __restrict__ xs, uint32_t* zero,
+                          int64_t zero_words) {
+    __shared__ uint32_t s_max[8];
+    __shared__ int s_idx[kSmallSlots];
+    __shared__ int s_dst[16];
+    grid_dependency_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int t = blockIdx.x, n = T * k;
+    for (int64_t i = (int64_t)t * kSmallThreads + tid; i < zero_words;
+         i += (int64_t)T * kSmallThreads)
+        zero[i] = 0u;
+    for (int j = tid; j < n; j += kSmallThreads) {
+        const int e = __ldg(idx + j);
+        s_idx[j] = e < E ? e : -1;
+    }
+    const uint4* src = x + (int64_t)t * units * 2;
+    uint4 v[NU > 0 ? NU : 1][2];
+    const Quant q = read_row<NU, false>(src, units, tid, kSmallThreads, v, s_max);
+    __syncthreads();
+    for (int s = warp; s < k; s += kSmallThreads / 32) {
+        const int j = t * k + s, e = s_idx[j];
+        int before = 0;
+        for (int i = lane; i < n; i += 32) {
+            const int o = s_idx[i];
+            before += (o >= 0 && o < e) || (o == e && i < j);
+        }
+        before = __reduce_add_sync(kAll, before);
+        if (lane == 0) {
+            s_dst[s] = e >= 0 ? before : -1;
+            inv[j] = e >= 0 ? before : -1;
+            if (e >= 0 && perm_tok) perm_tok[before] = t;
         }
     }
+    for (int e = t + warp * T; e <= E; e += T * (kSmallThreads / 32)) {
+        int below = 0;
+        for (int i = lane; i < n; i += 32) below += s_idx[i] >= 0 && s_idx[i] < e;
+        below = __reduce_add_sync(kAll, below);
+        if (lane == 0) offsets[e] = below;
+    }
+    __syncthreads();
+    for (int s = 0; s < k; ++s)
+        if (s_dst[s] >= 0)
+            write_row<NU>(src, units, tid, kSmallThreads, v, q, s_dst[s], xq, xs);
 }
 
 // A warp a row up to 1536 values, when there are rows for it: less than 8 warps of a
@@ -406,6 +480,38 @@ __global__ void __launch_bounds__(kIndexThreads, 1)
     sm100::cluster_sync_all();  // nobody leaves while its totals may still be read
 }
 
+int launch_index(const moe_shape& s, const int32_t* idx, int32_t* offsets, int32_t* perm_tok,
+                 int32_t* inv, cudaStream_t stream) {
+    if (s.E <= 32) return launch_dispatch_index(s, idx, offsets, perm_tok, inv, stream);
+    const int64_t n = (int64_t)s.T * s.k;
+    int C = 1;
+    while (C < kMaxCluster && n > (int64_t)C * kIndexWarps * kSlotsPerWarp) C *= 2;
+    const int smem = kIndexWarps * (s.E + 1) * 4;
+    int bits = 0;
+    while ((1 << bits) < s.E) ++bits;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(index_many_kernel),
+                             kIndexWarps * (kMaxE + 1) * 4))
+        return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kIndexThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, (int)n, (int)s.E, bits, (int)s.k, offsets,
+                              perm_tok, inv) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
 // ------------------------------------------------------------------ combine
 // One thread per (token, 8 columns); the k rows' loads are issued before any is used.
 template <int KMAX>
@@ -452,42 +558,26 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace int8rows
 
-int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* offsets,
-                               int32_t* perm_tok, int32_t* inv, cudaStream_t stream) {
+int launch_dispatch_quantize(const moe_shape& s, const int32_t* idx, const void* x,
+                             int32_t* offsets, int32_t* perm_tok, int32_t* inv, int8_t* xq,
+                             float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t stream) {
     using namespace int8rows;
-    if (s.E <= 32) return launch_dispatch_index(s, idx, offsets, perm_tok, inv, stream);
-    const int64_t n = (int64_t)s.T * s.k;
-    int C = 1;
-    while (C < kMaxCluster && n > (int64_t)C * kIndexWarps * kSlotsPerWarp) C *= 2;
-    const int smem = kIndexWarps * (s.E + 1) * 4;
-    int bits = 0;
-    while ((1 << bits) < s.E) ++bits;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(index_many_kernel),
-                             kIndexWarps * (kMaxE + 1) * 4))
-        return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kIndexThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, index_many_kernel, idx, (int)n, (int)s.E, bits, (int)s.k, offsets,
-                              perm_tok, inv) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
-}
-
-int launch_quantize_scatter(const moe_shape& s, const void* x, const int32_t* inv, int8_t* xq,
-                            float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t stream) {
-    return int8rows::launch_quantize<true>(x, s.T, s.d, inv, s.k, xq, xs, zero, zero_words, stream);
+    if (s.T > 0 && (int64_t)s.T * s.k <= kSmallSlots) {
+        const int units = s.d / 16;
+        const int per = (units + kSmallThreads - 1) / kSmallThreads;
+        auto kern = per <= 1   ? small_dispatch_kernel<1>
+                    : per <= 2 ? small_dispatch_kernel<2>
+                    : per <= 4 ? small_dispatch_kernel<4>
+                               : small_dispatch_kernel<0>;
+        return launch_pdl(kern, dim3(s.T), dim3(kSmallThreads), 0, stream, idx,
+                          static_cast<const uint4*>(x), s.T, s.E, s.k, units, offsets, perm_tok,
+                          inv, reinterpret_cast<uint4*>(xq), xs, zero, zero_words) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
+    }
+    const int rc = launch_index(s, idx, offsets, perm_tok, inv, stream);
+    if (rc || s.T == 0) return rc;
+    return launch_quantize<true>(x, s.T, s.d, inv, s.k, xq, xs, zero, zero_words, stream);
 }
 
 int launch_quantize_rows(const void* h, int max_rows, int cols, const int32_t* n_rows, int8_t* hq,

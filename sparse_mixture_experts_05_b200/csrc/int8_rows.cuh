@@ -9,14 +9,12 @@
 
 namespace moe {
 
-// offsets, perm_tok and inv of moe_dispatch for up to 512 experts and 16 slots.
-int launch_dispatch_index_many(const moe_shape& s, const int32_t* idx, int32_t* offsets,
-                               int32_t* perm_tok, int32_t* inv, cudaStream_t stream);
-
-// xq[inv[t, s]], xs[inv[t, s]] = row t of x quantised, for every slot s with a row.
+// offsets, perm_tok and inv of moe_dispatch for up to 512 experts and 16 slots, and the
+// rows of x quantised: xq[inv[t, s]], xs[inv[t, s]] for every slot s with a row.
 // Zeroes `zero_words` 32-bit words at `zero` on the way (may be none).
-int launch_quantize_scatter(const moe_shape& s, const void* x, const int32_t* inv, int8_t* xq,
-                            float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t stream);
+int launch_dispatch_quantize(const moe_shape& s, const int32_t* idx, const void* x,
+                             int32_t* offsets, int32_t* perm_tok, int32_t* inv, int8_t* xq,
+                             float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t stream);
 
 // hq[r], hs[r] = row r of h [max_rows, cols] quantised, for r < *n_rows.
 int launch_quantize_rows(const void* h, int max_rows, int cols, const int32_t* n_rows, int8_t* hq,
