@@ -480,11 +480,16 @@ int moe_dispatch_int8(moe_shape s, const int32_t* idx, const void* x, int32_t* o
  *   ws: >= moe_expert_swiglu_int8_workspace_bytes(s) bytes of device memory
  * The products are summed exactly in int32 and scaled in float32, row scale first;
  * h is rounded to bf16 (the layer's own precision for it) before its rows are
- * quantised, and o to bf16 (2^-9 against the 2^-8 and more of the 8-bit rows).
+ * quantised, and o to bf16 (each at most 2^-8 of a value, where the 8-bit rows are off
+ * by up to half of 1/127 of their largest).
  * Rows at or beyond offsets[E] are left untouched; an expert without rows costs
  * nothing; a row's result does not depend on the other rows.  A row whose
- * scale is NaN (x held an infinity or a NaN) gives NaN.  A device wait that
- * expires leaves o incomplete and is reported by moe_read_device_status(ws).
+ * scale is NaN (x held an infinity or a NaN) gives NaN, and so does a row with an a or
+ * an h past its type's range.  Only rows that offsets give to an expert are
+ * written, also if they do not ascend (which rows then hold what is open).  A device wait
+ * that expires leaves o incomplete and is reported by moe_read_device_status(ws).
+ * A workspace serves one call at a time: calls on one stream may share it, graphs
+ * among them.
  */
 size_t moe_expert_swiglu_int8_workspace_bytes(moe_shape s);
 int moe_expert_swiglu_int8(moe_shape s, const int8_t* xq, const float* xs,

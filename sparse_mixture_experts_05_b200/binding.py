@@ -173,11 +173,11 @@ def status_string(status: int) -> str:
 
 @functools.lru_cache(maxsize=1024)
 def _shape_of(T, d, d_ff, E, k) -> MoeShape:
-    return MoeShape(int(T), int(d), int(d_ff), int(E), int(k))
+    return MoeShape(T, d, d_ff, E, k)
 
 
 def _shape(shape) -> MoeShape:
-    return _shape_of(*shape)  # passed by value: one object serves every call of a shape
+    return _shape_of(*map(int, shape))  # passed by value: one object serves a shape's calls
 
 
 def _p(t):
@@ -639,6 +639,27 @@ def _given(t, name: str, like):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _queue(stream, device: int):
+    """The handle of `stream`, of the current device, or of its current stream."""
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, "
+                         f"the current device is cuda:{device}")
+    return _stream(stream)
+
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor of the stream that the work runs on, so that its memory is neither still in use
+    by another stream's work nor, once released, handed out before this work is done."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _scratch(nbytes: int, like, stream):
+    return _empty((max(nbytes, 256),), torch.uint8, like, stream)
+
+
 def _logits(t, shape, device: int):
     """(pointer, type code) of router logits."""
     kind = _LOGITS_TYPES.get(t.dtype)
@@ -676,13 +697,13 @@ def moe_route_scored(shape, logits, scoring: MoeScoring, bias=None, mask=None, i
     lp, kind = _logits(logits, shape, dev)
     bp = _arg(bias, "bias", torch.float32, (E,), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev)
-    idx = logits.new_empty((T, k), dtype=torch.int32) if idx is None else idx
-    gate = logits.new_empty((T, k), dtype=torch.float32) if gate is None else gate
+    idx = _empty((T, k), torch.int32, logits, stream) if idx is None else idx
+    gate = _empty((T, k), torch.float32, logits, stream) if gate is None else gate
     _check("moe_route_scored",
            lib().moe_route_scored(_shape(shape), scoring, lp, kind, bp, mp,
                                   _arg(idx, "idx", torch.int32, (T, k), dev),
                                   _arg(gate, "gate", torch.float32, (T, k), dev),
-                                  _stream(stream)))
+                                  _queue(stream, dev)))
     return idx, gate
 
 
@@ -697,11 +718,11 @@ def moe_route_scored_backward(shape, logits, scoring: MoeScoring, idx, dgate, dl
     lp, kind = _logits(logits, shape, dev)
     ip = _arg(idx, "idx", torch.int32, (T, k), dev)
     gp = _arg(dgate, "dgate", torch.float32, (T, k), dev)
-    dlogits = torch.empty_like(logits) if dlogits is None else dlogits
+    dlogits = _empty((T, E), logits.dtype, logits, stream) if dlogits is None else dlogits
     _check("moe_route_scored_backward",
            lib().moe_route_scored_backward(_shape(shape), scoring, lp, kind, ip, gp,
                                            _arg(dlogits, "dlogits", logits.dtype, (T, E), dev),
-                                           _stream(stream)))
+                                           _queue(stream, dev)))
     return dlogits
 
 
@@ -714,12 +735,12 @@ def moe_quantize_weights_int8(W, Wq=None, scale=None, stream=None):
     E, K, N = W.shape
     dev = torch.cuda.current_device()
     wp = _arg(W, "W", torch.bfloat16, (E, K, N), dev)
-    Wq = W.new_empty((E, N, K), dtype=torch.int8) if Wq is None else Wq
-    scale = W.new_empty((E, N), dtype=torch.float32) if scale is None else scale
+    Wq = _empty((E, N, K), torch.int8, W, stream) if Wq is None else Wq
+    scale = _empty((E, N), torch.float32, W, stream) if scale is None else scale
     _check("moe_quantize_weights_int8",
            lib().moe_quantize_weights_int8(E, K, N, wp, _arg(Wq, "Wq", torch.int8, (E, N, K), dev),
                                            _arg(scale, "scale", torch.float32, (E, N), dev),
-                                           _stream(stream)))
+                                           _queue(stream, dev)))
     return Wq, scale
 
 
@@ -732,18 +753,19 @@ def moe_dispatch_int8(shape, idx, x, offsets=None, perm_tok=None, inv=None, xq=N
     dev = torch.cuda.current_device()
     ip = _arg(idx, "idx", torch.int32, (T, k), dev)
     xp = _arg(x, "x", torch.bfloat16, (T, d), dev)
-    offsets = x.new_empty((E + 1,), dtype=torch.int32) if offsets is None else offsets
-    perm_tok = x.new_empty((T * k,), dtype=torch.int32) if perm_tok is None else perm_tok
-    inv = x.new_empty((T, k), dtype=torch.int32) if inv is None else inv
-    xq = x.new_empty((T * k, d), dtype=torch.int8) if xq is None else xq
-    xs = x.new_empty((T * k,), dtype=torch.float32) if xs is None else xs
+    offsets = _empty((E + 1,), torch.int32, x, stream) if offsets is None else offsets
+    perm_tok = _empty((T * k,), torch.int32, x, stream) if perm_tok is None else perm_tok
+    inv = _empty((T, k), torch.int32, x, stream) if inv is None else inv
+    xq = _empty((T * k, d), torch.int8, x, stream) if xq is None else xq
+    xs = _empty((T * k,), torch.float32, x, stream) if xs is None else xs
     _check("moe_dispatch_int8",
            lib().moe_dispatch_int8(_shape(shape), ip, xp,
                                    _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
                                    _arg(perm_tok, "perm_tok", torch.int32, (T * k,), dev),
                                    _arg(inv, "inv", torch.int32, (T, k), dev),
                                    _arg(xq, "xq", torch.int8, (T * k, d), dev),
-                                   _arg(xs, "xs", torch.float32, (T * k,), dev), _stream(stream)))
+                                   _arg(xs, "xs", torch.float32, (T * k,), dev),
+                                   _queue(stream, dev)))
     return offsets, perm_tok, inv, xq, xs
 
 
@@ -764,14 +786,14 @@ def _ws_arg(ws, device: int):
     return _arg(ws, "ws", torch.uint8, ws.shape, device), ws.numel()
 
 
-def _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws):
+def _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws, stream):
     T, d, d_ff, E, k = shape
     R = T * k
     _given(xq, "xq", xq)
     dev = torch.cuda.current_device()
-    o = xq.new_empty((R, d), dtype=torch.bfloat16) if o is None else o
+    o = _empty((R, d), torch.bfloat16, xq, stream) if o is None else o
     if ws is None:
-        ws = workspace(moe_expert_swiglu_int8_workspace_bytes(shape), xq.device)
+        ws = _scratch(moe_expert_swiglu_int8_workspace_bytes(shape), xq, stream)
     args = (_arg(xq, "xq", torch.int8, (R, d), dev), _arg(xs, "xs", torch.float32, (R,), dev),
             _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
             *_int8_weights(shape, W1, W3, W2, dev), _arg(o, "o", torch.bfloat16, (R, d), dev),
@@ -784,18 +806,19 @@ def moe_expert_swiglu_int8(shape, xq, xs, offsets, W1, W3, W2, o=None, ws=None, 
 
     W1, W3, W2 are the (int8, scale) pairs of moe_quantize_weights_int8.  Returns
     (o [T*k, d] bfloat16, ws)."""
-    args, o, ws = _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws)
+    args, o, ws = _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws, stream)
     _check("moe_expert_swiglu_int8",
-           lib().moe_expert_swiglu_int8(_shape(shape), *args, _stream(stream)))
+           lib().moe_expert_swiglu_int8(_shape(shape), *args, _queue(stream, xq.get_device())))
     return o, ws
 
 
 def moe_expert_swiglu_int8_stall_test(shape, xq, xs, offsets, W1, W3, W2, stall_after: int,
                                       timeout_ns: int, o=None, ws=None, stream=None):
-    args, o, ws = _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws)
+    args, o, ws = _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws, stream)
     _check("moe_expert_swiglu_int8_stall_test",
            lib().moe_expert_swiglu_int8_stall_test(_shape(shape), *args, int(stall_after),
-                                                   int(timeout_ns), _stream(stream)))
+                                                   int(timeout_ns),
+                                                   _queue(stream, xq.get_device())))
     return o, ws
 
 
@@ -804,12 +827,12 @@ def moe_combine_bf16(shape, o, inv, gate, y=None, stream=None):
     T, d, d_ff, E, k = shape
     _given(o, "o", o)
     dev = torch.cuda.current_device()
-    y = o.new_empty((T, d)) if y is None else y
+    y = _empty((T, d), torch.bfloat16, o, stream) if y is None else y
     _check("moe_combine_bf16",
            lib().moe_combine_bf16(_shape(shape), _arg(o, "o", torch.bfloat16, (T * k, d), dev),
                                   _arg(inv, "inv", torch.int32, (T, k), dev),
                                   _arg(gate, "gate", torch.float32, (T, k), dev),
-                                  _arg(y, "y", torch.bfloat16, (T, d), dev), _stream(stream)))
+                                  _arg(y, "y", torch.bfloat16, (T, d), dev), _queue(stream, dev)))
     return y
 
 
@@ -823,8 +846,8 @@ def moe_forward_int8(shape, x, logits, scoring: MoeScoring, W1, W3, W2, route_bi
     _given(logits, "logits", logits)
     dev = torch.cuda.current_device()
     lp, kind = _logits(logits, shape, dev)
-    y = torch.empty_like(x) if y is None else y
-    ws = workspace(moe_forward_int8_workspace_bytes(shape), x.device) if ws is None else ws
+    y = _empty((T, d), torch.bfloat16, x, stream) if y is None else y
+    ws = _scratch(moe_forward_int8_workspace_bytes(shape), x, stream) if ws is None else ws
     _check("moe_forward_int8",
            lib().moe_forward_int8(_shape(shape), _arg(x, "x", torch.bfloat16, (T, d), dev), lp, kind,
                                   scoring, _arg(route_bias, "route_bias", torch.float32, (E,), dev),
@@ -833,5 +856,5 @@ def moe_forward_int8(shape, x, logits, scoring: MoeScoring, W1, W3, W2, route_bi
                                   _arg(y, "y", torch.bfloat16, (T, d), dev),
                                   _arg(idx_out, "idx_out", torch.int32, (T, k), dev),
                                   _arg(gate_out, "gate_out", torch.float32, (T, k), dev),
-                                  *_ws_arg(ws, dev), _stream(stream)))
+                                  *_ws_arg(ws, dev), _queue(stream, dev)))
     return y

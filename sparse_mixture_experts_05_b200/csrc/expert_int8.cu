@@ -83,13 +83,15 @@ struct Params {
 };
 
 // Offsets, held to 0 .. R so that no tile lies outside the R rows, and the exclusive
-// prefix over the experts of their m-tiles of `rows` rows.  All threads of the CTA.
+// prefix over the experts of their m-tiles of `rows` rows, held to the most that
+// ascending offsets can give (what the counters have room for).  All threads of the CTA.
 __device__ __forceinline__ void tile_prefix(const int32_t* offsets, int E, int R, int rows,
                                             int* s_off, int* s_mt) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) s_off[e] = min(max(offsets[e], 0), R);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
+        const int most = R / rows + min(R, E);
         int carry = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
@@ -100,10 +102,10 @@ __device__ __forceinline__ void tile_prefix(const int32_t* offsets, int E, int R
                 const int o = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += o;
             }
-            if (e < E) s_mt[e] = carry + incl - mine;
+            if (e < E) s_mt[e] = min(carry + incl - mine, most);
             carry += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (lane == 0) s_mt[E] = carry;
+        if (lane == 0) s_mt[E] = min(carry, most);
     }
 }
 

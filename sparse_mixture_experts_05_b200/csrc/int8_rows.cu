@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         if (lane == 0) {
             s_dst[s] = e >= 0 ? before : -1;
             inv[j] = e >= 0 ? before : -1;
-            if (e >= 0 && perm_tok) perm_tok[before] = t;
+            if (e >= 0) perm_tok[before] = t;
         }
     }
     for (int e = t + warp * T; e <= E; e += T * (kSmallThreads / 32)) {
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(256)
 // shared memory.  The warps take the experts in turn and scan an expert's counters
 // over the CTA's 32 warps; thread e reads the other CTAs' totals of expert e through
 // distributed shared memory, and a scan over the experts gives their first rows.
-// Stable, deterministic, no atomics on positions.  perm_tok may be null.
+// Stable, deterministic, no atomics on positions.
 constexpr int kIndexThreads = 1024;
 constexpr int kIndexWarps = 32;
 constexpr int kMaxE = 512;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kIndexThreads, 1)
             int p = -1;
             if (e >= 0) {
                 p = pos[e] + s_base[e] + __popc(same & lt);
-                if (perm_tok) perm_tok[p] = j / k;
+                perm_tok[p] = j / k;
             }
             if (j < j1) inv[j] = p;
             __syncwarp();

@@ -311,3 +311,181 @@ def test_expired_waits_are_reported_and_the_next_call_is_exact(T):
     o, _ = moe.moe_expert_swiglu_int8(shape, xq, xs, offsets, *weights, ws=ws)
     assert moe.moe_read_device_status(ws) == moe.MOE_OK
     assert torch.equal(o, want)
+
+
+# ------------------------------------------------------------------ borders
+
+@pytest.mark.parametrize("T,E,k", [(1024, 8, 1), (1025, 8, 1), (128, 32, 8), (205, 32, 5), (128, 33, 8),
+                                   (205, 33, 5), (64, 512, 16), (65, 512, 16), (2, 40, 16)])
+def test_dispatch_where_the_kernels_change(T, E, k):
+    """1024 slots and one more, 32 experts and one more, the most experts and slots."""
+    x, idx = _x(T, 64, 1), _idx(T, E, k, 2)
+    offsets, perm, inv, xq, xs = moe.moe_dispatch_int8((T, 64, 128, E, k), idx, x)
+    r_off, r_perm, r_inv = ref.dispatch(idx, E)
+    assert np.array_equal(offsets.cpu().numpy(), r_off)
+    assert np.array_equal(perm.cpu().numpy(), r_perm)
+    assert np.array_equal(inv.cpu().numpy(), r_inv)
+    q, s = ref.quantize(x)
+    rows = torch.as_tensor(r_perm, device="cuda")
+    assert torch.equal(xq.double(), q[rows]) and torch.equal(xs, s[rows])
+
+
+@pytest.mark.parametrize("shape", [(511, 192, 160, 7, 1), (256, 192, 160, 7, 2), (400, 3520, 144, 2, 2),
+                                   (1600, 3520, 3520, 1, 1)], ids=str)
+def test_products_where_the_plans_change(shape):
+    """511 and 512 rows; K on both sides of the pairs' rule, for both products."""
+    T, d, d_ff, E, k = shape
+    _check_experts(shape, _idx(T, E, k, 5), _x(T, d, 6), ref.random_weights(E, d, d_ff, 7))
+
+
+@pytest.mark.parametrize("T", [12, 640])
+def test_a_batch_of_nothing_but_padding(T):
+    shape = (T, 256, 512, 8, 2)
+    weights = ref.random_weights(8, 256, 512, 3)
+    ws = moe.workspace(moe.moe_forward_int8_workspace_bytes(shape), "cuda").fill_(255)
+    x = torch.full((T, 256), float("nan"), device="cuda").bfloat16()
+    y = moe.moe_forward_int8(shape, x, torch.full((T, 8), float("nan"), device="cuda"),
+                             moe.MoeScoring(), *weights, ws=ws,
+                             mask=torch.zeros(T, dtype=torch.uint8, device="cuda"))
+    assert torch.all(y == 0)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [24, 700])
+def test_offsets_that_do_not_ascend_stay_within_the_buffers(T):
+    shape = (T, 256, 400, 8, 2)
+    R = 2 * T
+    weights = ref.random_weights(8, 256, 400, 3)
+    idx, x = _idx(T, 8, 2, 1), _x(T, 256, 2)
+    offsets, _, _, xq, xs = moe.moe_dispatch_int8(shape, idx, x)
+    n = moe.moe_expert_swiglu_int8_workspace_bytes(shape)
+    ws = torch.full((n + 4096,), 77, dtype=torch.uint8, device="cuda")
+    o = torch.full((R + 8, 256), -7.0, dtype=torch.bfloat16, device="cuda")
+    for wild in ([0, R, 0, R, 0, R, 0, R, 0], [-5, 3 * R, R // 2, -(1 << 31), (1 << 31) - 1, 0, 7, R, 1 << 30]):
+        wild = torch.tensor(wild, dtype=torch.int32, device="cuda")
+        moe.moe_expert_swiglu_int8(shape, xq, xs, wild, *weights, o=o[:R], ws=ws[:n])
+        assert moe.moe_read_device_status(ws) == moe.MOE_OK
+        assert torch.all(o[R:] == -7.0) and torch.all(ws[n:] == 77)
+    want, _ = moe.moe_expert_swiglu_int8(shape, xq, xs, offsets, *weights)
+    got, _ = moe.moe_expert_swiglu_int8(shape, xq, xs, offsets, *weights, ws=ws[:n])
+    assert torch.equal(got, want)
+
+
+def test_rows_past_32_bit_offsets():
+    """Rows whose values lie past 2^31 elements and 2^32 bytes, of every tensor of the
+    layer: the last tokens have the bits that they have alone."""
+    T, n = 530000, 200
+    shape = (T, 4096, 4096, 2, 2)
+    weights = ref.random_weights(2, 4096, 4096, 3)
+    x = torch.zeros(T, 4096, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = _x(n, 4096, 1)
+    logits = torch.randn(T, 2, generator=_gen(2), device="cuda")
+    sc = moe.MoeScoring(score="sigmoid", renorm=False)
+    y = moe.moe_forward_int8(shape, x, logits, sc, *weights)
+    one = moe.moe_forward_int8((n, 4096, 4096, 2, 2), x[-n:].clone(), logits[-n:].clone(), sc, *weights)
+    assert torch.equal(y[-n:], one)
+    assert not torch.any(y[:-n]) and torch.any(one != 0)
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_weights_past_32_bit_offsets(T):
+    """An expert whose weights begin past 2^31 bytes, against the same weights alone."""
+    E, d, d_ff = 40, 4096, 14336
+    last = [moe.moe_quantize_weights_int8((0.02 * torch.randn(1, a, b, generator=_gen(i), device="cuda")).bfloat16())
+            for i, (a, b) in enumerate(((d, d_ff), (d, d_ff), (d_ff, d)))]
+    weights = []
+    for q, s in last:
+        Q = torch.zeros(E, *q.shape[1:], dtype=torch.int8, device="cuda")
+        S = torch.zeros(E, s.shape[1], device="cuda")
+        Q[-1], S[-1] = q[0], s[0]
+        weights.append((Q, S))
+    x = _x(T, d, 9)
+    outs = []
+    for experts, w in ((E, weights), (1, last)):
+        shape = (T, d, d_ff, experts, 1)
+        idx = torch.full((T, 1), experts - 1, dtype=torch.int32, device="cuda")
+        offsets, _, _, xq, xs = moe.moe_dispatch_int8(shape, idx, x)
+        outs.append(moe.moe_expert_swiglu_int8(shape, xq, xs, offsets, *w)[0])
+    assert torch.equal(*outs) and torch.any(outs[0] != 0)
+    W = torch.zeros(E, d, d_ff, dtype=torch.bfloat16, device="cuda")     # 2^32 bytes and more
+    W[-1] = _x(d, d_ff, 4)
+    q, s = moe.moe_quantize_weights_int8(W)
+    q1, s1 = moe.moe_quantize_weights_int8(W[-1:].clone())
+    assert torch.equal(q[-1], q1[0]) and torch.equal(s[-1], s1[0]) and not torch.any(q[:-1])
+
+
+# ------------------------------------------------------------------ how it is called
+
+def test_memory_of_a_call_on_another_stream_is_not_handed_out_early():
+    shape = (16, 256, 512, 8, 2)
+    weights = ref.random_weights(8, 256, 512, 3)
+    x, l = _x(16, 256, 1), torch.randn(16, 8, generator=_gen(2), device="cuda")
+    sc = moe.MoeScoring()
+    want = moe.moe_forward_int8(shape, x, l, sc, *weights)
+    nbytes = moe.moe_forward_int8_workspace_bytes(shape)
+    stream = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(20_000_000)            # the call's kernels begin later
+        y = moe.moe_forward_int8(shape, x, l, sc, *weights, stream=stream)
+        junk = [moe.workspace(nbytes, "cuda").fill_(255) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del junk
+
+
+@pytest.mark.parametrize("T", [16, 700])
+def test_two_graphs_share_a_workspace(T):
+    sc = moe.MoeScoring(score="sigmoid")
+    shapes = [(T, 256, 512, 8, 2), (T // 2, 256, 512, 8, 2)]
+    weights = ref.random_weights(8, 256, 512, 3)
+    ws = moe.workspace(moe.moe_forward_int8_workspace_bytes(shapes[0]), "cuda").fill_(255)
+    runs = []
+    for s in shapes:
+        x, l = _x(s[0], 256, s[0]), torch.randn(s[0], 8, generator=_gen(s[0]), device="cuda")
+        want = moe.moe_forward_int8(s, x, l, sc, *weights)
+        y = torch.empty_like(x)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_forward_int8(s, x, l, sc, *weights, y=y, ws=ws)
+        runs.append((graph, x, l, y, want))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        graph, _, _, y, want = runs[i]
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+_FIRST_CALL = """
+import torch
+import sparse_mixture_experts_05_b200 as moe
+T, d, d_ff, E, k = shape = (%d, 256, 512, 64, 4)
+g = torch.Generator("cuda").manual_seed(1)
+W = [(torch.randint(-127, 128, (E, b, a), generator=g, device="cuda").to(torch.int8),
+      torch.rand(E, b, generator=g, device="cuda")) for a, b in ((d, d_ff), (d, d_ff), (d_ff, d))]
+x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+l = torch.randn(T, E, generator=g, device="cuda")
+ws = moe.workspace(moe.moe_forward_int8_workspace_bytes(shape), "cuda")
+y = torch.empty_like(x)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    moe.moe_forward_int8(shape, x, l, moe.MoeScoring(), *W, y=y, ws=ws)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, moe.moe_forward_int8(shape, x, l, moe.MoeScoring(), *W))
+assert torch.any(y != 0)
+"""
+
+
+@pytest.mark.parametrize("T", [16, 700])
+def test_a_process_may_begin_with_a_capture(T):
+    import pathlib
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", _FIRST_CALL % T], capture_output=True, text=True, timeout=300,
+                         cwd=pathlib.Path(__file__).resolve().parent.parent)
+    assert out.returncode == 0, out.stderr[-2000:]

@@ -218,3 +218,19 @@ def test_reference_gradient_by_autograd():
             (2.0 * w * dg.double()).sum().backward()
             got, _ = ref.route_backward(l, torch.as_tensor(idx), dg, sc)
             assert np.allclose(got, x.grad.numpy(), rtol=1e-9, atol=1e-12)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+    with pytest.raises(ValueError, match="cuda:1"):
+        binding._queue(Stream(), 0)
+    assert binding._queue(Stream(), 1) == 0
+
+
+def test_a_shape_is_read_anew_by_every_call():
+    T = torch.tensor(4)
+    shape = [T, 128, np.int64(128), 8, 2]
+    assert binding._shape(shape).T == 4
+    T.add_(1)
+    assert binding._shape(shape).T == 5
