@@ -656,6 +656,14 @@ def _empty(shape, dtype, like, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _out(t, name: str, dtype, shape, like, stream, device: int):
+    """An output and its pointer: the caller's, checked, or a new one."""
+    if t is None:
+        t = _empty(shape, dtype, like, stream)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, device)
+
+
 def _scratch(nbytes: int, like, stream):
     return _empty((max(nbytes, 256),), torch.uint8, like, stream)
 
@@ -697,12 +705,10 @@ def moe_route_scored(shape, logits, scoring: MoeScoring, bias=None, mask=None, i
     lp, kind = _logits(logits, shape, dev)
     bp = _arg(bias, "bias", torch.float32, (E,), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev)
-    idx = _empty((T, k), torch.int32, logits, stream) if idx is None else idx
-    gate = _empty((T, k), torch.float32, logits, stream) if gate is None else gate
+    idx, ip = _out(idx, "idx", torch.int32, (T, k), logits, stream, dev)
+    gate, gp = _out(gate, "gate", torch.float32, (T, k), logits, stream, dev)
     _check("moe_route_scored",
-           lib().moe_route_scored(_shape(shape), scoring, lp, kind, bp, mp,
-                                  _arg(idx, "idx", torch.int32, (T, k), dev),
-                                  _arg(gate, "gate", torch.float32, (T, k), dev),
+           lib().moe_route_scored(_shape(shape), scoring, lp, kind, bp, mp, ip, gp,
                                   _queue(stream, dev)))
     return idx, gate
 
@@ -718,10 +724,9 @@ def moe_route_scored_backward(shape, logits, scoring: MoeScoring, idx, dgate, dl
     lp, kind = _logits(logits, shape, dev)
     ip = _arg(idx, "idx", torch.int32, (T, k), dev)
     gp = _arg(dgate, "dgate", torch.float32, (T, k), dev)
-    dlogits = _empty((T, E), logits.dtype, logits, stream) if dlogits is None else dlogits
+    dlogits, dp = _out(dlogits, "dlogits", logits.dtype, (T, E), logits, stream, dev)
     _check("moe_route_scored_backward",
-           lib().moe_route_scored_backward(_shape(shape), scoring, lp, kind, ip, gp,
-                                           _arg(dlogits, "dlogits", logits.dtype, (T, E), dev),
+           lib().moe_route_scored_backward(_shape(shape), scoring, lp, kind, ip, gp, dp,
                                            _queue(stream, dev)))
     return dlogits
 
@@ -735,12 +740,10 @@ def moe_quantize_weights_int8(W, Wq=None, scale=None, stream=None):
     E, K, N = W.shape
     dev = torch.cuda.current_device()
     wp = _arg(W, "W", torch.bfloat16, (E, K, N), dev)
-    Wq = _empty((E, N, K), torch.int8, W, stream) if Wq is None else Wq
-    scale = _empty((E, N), torch.float32, W, stream) if scale is None else scale
+    Wq, qp = _out(Wq, "Wq", torch.int8, (E, N, K), W, stream, dev)
+    scale, sp = _out(scale, "scale", torch.float32, (E, N), W, stream, dev)
     _check("moe_quantize_weights_int8",
-           lib().moe_quantize_weights_int8(E, K, N, wp, _arg(Wq, "Wq", torch.int8, (E, N, K), dev),
-                                           _arg(scale, "scale", torch.float32, (E, N), dev),
-                                           _queue(stream, dev)))
+           lib().moe_quantize_weights_int8(E, K, N, wp, qp, sp, _queue(stream, dev)))
     return Wq, scale
 
 
@@ -753,19 +756,13 @@ def moe_dispatch_int8(shape, idx, x, offsets=None, perm_tok=None, inv=None, xq=N
     dev = torch.cuda.current_device()
     ip = _arg(idx, "idx", torch.int32, (T, k), dev)
     xp = _arg(x, "x", torch.bfloat16, (T, d), dev)
-    offsets = _empty((E + 1,), torch.int32, x, stream) if offsets is None else offsets
-    perm_tok = _empty((T * k,), torch.int32, x, stream) if perm_tok is None else perm_tok
-    inv = _empty((T, k), torch.int32, x, stream) if inv is None else inv
-    xq = _empty((T * k, d), torch.int8, x, stream) if xq is None else xq
-    xs = _empty((T * k,), torch.float32, x, stream) if xs is None else xs
+    offsets, op = _out(offsets, "offsets", torch.int32, (E + 1,), x, stream, dev)
+    perm_tok, pp = _out(perm_tok, "perm_tok", torch.int32, (T * k,), x, stream, dev)
+    inv, vp = _out(inv, "inv", torch.int32, (T, k), x, stream, dev)
+    xq, qp = _out(xq, "xq", torch.int8, (T * k, d), x, stream, dev)
+    xs, sp = _out(xs, "xs", torch.float32, (T * k,), x, stream, dev)
     _check("moe_dispatch_int8",
-           lib().moe_dispatch_int8(_shape(shape), ip, xp,
-                                   _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-                                   _arg(perm_tok, "perm_tok", torch.int32, (T * k,), dev),
-                                   _arg(inv, "inv", torch.int32, (T, k), dev),
-                                   _arg(xq, "xq", torch.int8, (T * k, d), dev),
-                                   _arg(xs, "xs", torch.float32, (T * k,), dev),
-                                   _queue(stream, dev)))
+           lib().moe_dispatch_int8(_shape(shape), ip, xp, op, pp, vp, qp, sp, _queue(stream, dev)))
     return offsets, perm_tok, inv, xq, xs
 
 
@@ -791,13 +788,12 @@ def _int8_expert_args(shape, xq, xs, offsets, W1, W3, W2, o, ws, stream):
     R = T * k
     _given(xq, "xq", xq)
     dev = torch.cuda.current_device()
-    o = _empty((R, d), torch.bfloat16, xq, stream) if o is None else o
+    o, op = _out(o, "o", torch.bfloat16, (R, d), xq, stream, dev)
     if ws is None:
         ws = _scratch(moe_expert_swiglu_int8_workspace_bytes(shape), xq, stream)
     args = (_arg(xq, "xq", torch.int8, (R, d), dev), _arg(xs, "xs", torch.float32, (R,), dev),
             _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-            *_int8_weights(shape, W1, W3, W2, dev), _arg(o, "o", torch.bfloat16, (R, d), dev),
-            *_ws_arg(ws, dev))
+            *_int8_weights(shape, W1, W3, W2, dev), op, *_ws_arg(ws, dev))
     return args, o, ws
 
 
@@ -827,12 +823,12 @@ def moe_combine_bf16(shape, o, inv, gate, y=None, stream=None):
     T, d, d_ff, E, k = shape
     _given(o, "o", o)
     dev = torch.cuda.current_device()
-    y = _empty((T, d), torch.bfloat16, o, stream) if y is None else y
+    y, yp = _out(y, "y", torch.bfloat16, (T, d), o, stream, dev)
     _check("moe_combine_bf16",
            lib().moe_combine_bf16(_shape(shape), _arg(o, "o", torch.bfloat16, (T * k, d), dev),
                                   _arg(inv, "inv", torch.int32, (T, k), dev),
                                   _arg(gate, "gate", torch.float32, (T, k), dev),
-                                  _arg(y, "y", torch.bfloat16, (T, d), dev), _queue(stream, dev)))
+                                  yp, _queue(stream, dev)))
     return y
 
 
@@ -846,15 +842,14 @@ def moe_forward_int8(shape, x, logits, scoring: MoeScoring, W1, W3, W2, route_bi
     _given(logits, "logits", logits)
     dev = torch.cuda.current_device()
     lp, kind = _logits(logits, shape, dev)
-    y = _empty((T, d), torch.bfloat16, x, stream) if y is None else y
+    y, yp = _out(y, "y", torch.bfloat16, (T, d), x, stream, dev)
     ws = _scratch(moe_forward_int8_workspace_bytes(shape), x, stream) if ws is None else ws
     _check("moe_forward_int8",
            lib().moe_forward_int8(_shape(shape), _arg(x, "x", torch.bfloat16, (T, d), dev), lp, kind,
                                   scoring, _arg(route_bias, "route_bias", torch.float32, (E,), dev),
                                   _arg(mask, "mask", torch.uint8, (T,), dev),
                                   *_int8_weights(shape, W1, W3, W2, dev),
-                                  _arg(y, "y", torch.bfloat16, (T, d), dev),
-                                  _arg(idx_out, "idx_out", torch.int32, (T, k), dev),
+                                  yp, _arg(idx_out, "idx_out", torch.int32, (T, k), dev),
                                   _arg(gate_out, "gate_out", torch.float32, (T, k), dev),
                                   *_ws_arg(ws, dev), _queue(stream, dev)))
     return y
