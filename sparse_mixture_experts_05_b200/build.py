@@ -11,6 +11,7 @@ import argparse
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,9 +19,11 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "router.cu", "dispatch.cu", "expert_gemm.cu", "combine.cu", "aux_loss.cu",
-           "tma_map.cu", "api_int8.cu", "route_scored.cu", "int8_rows.cu", "expert_int8.cu"]
+           "tma_map.cu", "api_int8.cu", "route_scored.cu", "route_scored_bf16.cu",
+           "int8_rows.cu", "expert_int8.cu"]
 HEADERS = ["common.cuh", "sm100.cuh", "expert_gemm.cuh", "router.cuh", "dispatch.cuh",
-           "combine.cuh", "combine_math.cuh", "aux_loss.cuh", "tma_map.cuh", "route_scored.cuh", "int8_rows.cuh", "expert_int8.cuh"]
+           "combine.cuh", "combine_math.cuh", "aux_loss.cuh", "tma_map.cuh", "route_scored.cuh",
+           "route_scored_kernels.cuh", "int8_rows.cuh", "expert_int8.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -38,7 +41,7 @@ def _stale(target: str, deps: list[str]) -> bool:
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "moe.h")]
-    objs = []
+    objs, cmds = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -47,7 +50,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             cmd = [NVCC, *ARCH, *FLAGS, "-c", s, "-o", o]
             if verbose_ptxas:
                 cmd.insert(1, "-Xptxas=-v")
-            subprocess.check_call(cmd)
+            cmds.append(cmd)
+    with ThreadPoolExecutor(os.cpu_count() or 1) as pool:  # one nvcc a source, side by side
+        list(pool.map(subprocess.check_call, cmds))
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         subprocess.check_call([NVCC, *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp])

@@ -170,6 +170,27 @@ def test_logits_of_every_size(score, tops, scale, dtype):
     _check(l, 6, sc, torch.linspace(-0.3, 0.3, E, device="cuda"))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(64, 6, 1), (64, 6, 16), (256, 8, 8), (256, 8, 1), (40, 12, 5), (24, 2, 4),
+                                        (512, 16, 32), (8, 2, 1)])
+@pytest.mark.parametrize("levels", [2, 9, 40])
+def test_rows_with_many_nearly_equal_choices(score, E, k, groups, levels):
+    """A few levels of logits, equal or a few units of the last place apart, some experts
+    masked out: ties at the k-th place, between groups, and within their best two."""
+    gen = torch.Generator("cuda").manual_seed(levels)
+    T = 33
+    level = 1.0 + torch.randn(levels, generator=gen, device="cuda")
+    l = level[torch.randint(levels, (T, E), generator=gen, device="cuda")]
+    l = l * (1.0 + 2.0 ** -23 * torch.randint(-2, 3, (T, E), generator=gen, device="cuda"))
+    l[3, ::3] = -INF
+    l[4, E // 8:] = -INF
+    bias = 2.0 ** -3 * torch.randint(0, 3, (E,), generator=gen, device="cuda").float()
+    for top in (1, 2):
+        sc = dict(score=score, n_group=groups, topk_group=(groups + 1) // 2, group_top=top)
+        for b in (None, bias, torch.zeros(E, device="cuda")):
+            _check(l, k, sc, b)
+
+
 def test_equal_choices_go_to_the_lower_index():
     l = torch.zeros(3, 256, device="cuda")
     l[1, 100:] = 1.0
