@@ -53,12 +53,17 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // the previous kernel wrote and before any early exit: it returns once the
 // previous grid has completed and its memory operations are visible, so
 // completion of a kernel still implies completion of everything before it in
-// the stream.  Launched without the attribute, the wait returns at once.  No
-// kernel triggers its dependents early (griddepcontrol.launch_dependents):
-// waiting CTAs of the next kernel then sat on the SMs during the whole launch,
-// which measured slower at T = 4096.
+// the stream.  Launched without the attribute, the wait returns at once.  One
+// kernel triggers its dependents early (launch_dependents: the quantisation of h's
+// rows in 8 bits, see expert_int8.cu); elsewhere waiting CTAs of the next kernel then sat
+// on the SMs during the whole launch, which measured slower at T = 4096.
 __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the CTAs of the stream's next kernel start once every CTA of this grid has come here.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Raises `kernel`'s dynamic shared-memory limit to at least `bytes` on the

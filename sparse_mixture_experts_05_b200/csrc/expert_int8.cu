@@ -48,7 +48,7 @@ using namespace sm100;
 constexpr int kBM = 128;                            // rows of a tile (TMEM lanes)
 constexpr int kBK = 128;                            // values (= bytes) of K per stage
 constexpr int kAccCols = 256;                       // B rows of a tile
-constexpr int kStages = 4;
+constexpr int kStages = 4;  // with few rows 5 or 6 fit: no faster (16 tokens 250 us either way)
 constexpr int kABytes = kBM * kBK;                  // 16 KB
 constexpr int kBHalf = (kAccCols / 2) * kBK;        // 16 KB: one box of 128 B rows
 constexpr int kStageBytes = kABytes + 2 * kBHalf;   // 48 KB
@@ -87,7 +87,7 @@ struct Params {
 // ascending offsets can give (what the counters have room for).  All threads of the CTA.
 __device__ __forceinline__ void tile_prefix(const int32_t* offsets, int E, int R, int rows,
                                             int* s_off, int* s_mt) {
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) s_off[e] = min(max(offsets[e], 0), R);
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) s_off[e] = min(max(__ldcg(offsets + e), 0), R);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -442,7 +442,9 @@ struct Run {
 // ------------------------------------------------------------------ the kernel
 // Roles (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer, the
 // others epilogue.  Four stages of 48 KB; two TMEM accumulators,
-// so that a tile's epilogue overlaps the next tile's products.
+// so that a tile's epilogue overlaps the next tile's products.  The down product's weights
+// depend on nothing that the kernel before it (h's quantisation) writes, nor do the offsets:
+// its producers load the first stages' weights before they wait for that kernel.
 template <bool kSwiGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&tmem_slot, kTmemCols);
         tmem_relinquish();
     }
-    grid_dependency_wait();
+    if (kSwiGLU) grid_dependency_wait();  // the down product waits further below
     tile_prefix(p.offsets, p.E, p.R, kBM, s_off, s_mt);
     tc_fence_before_sync();
     __syncthreads();
@@ -490,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb_count = (p.K + kBK - 1) / kBK;
     Run run(blockIdx.x, gridDim.x, s_mt[p.E] * n_tiles, kb_count, p.may_cut != 0,
             p.cut_units);
+    if (!kSwiGLU && warp != 0) grid_dependency_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -497,6 +500,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0, issued = 0, e = 0;
             uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
             bool ok = true;
+            int ahead = 0;  // stages whose weights are on their way already
+            if constexpr (!kSwiGLU) {
+                Run begin = run;
+                if (p.stall_after < 0 && begin.next()) {
+                    const Tile ti = locate(begin.t, e, s_mt, s_off, n_tiles, kTileCols, kBM,
+                                           p.group_m);
+                    for (; ahead < kStages && begin.kb0 + ahead < begin.kb1; ++ahead) {
+                        uint8_t* sB = smem + ahead * kStageBytes + kABytes;
+                        const int x = (begin.kb0 + ahead) * kBK;
+                        mbar_arrive_expect_tx(&full_bar[ahead], p.a_rows * kBK + 2 * kBHalf);
+                        tma_load_3d(sB, &tmB0, &full_bar[ahead], x, ti.n0, ti.e);
+                        tma_load_3d(sB + kBHalf, &tmB0, &full_bar[ahead], x,
+                                    ti.n0 + kAccCols / 2, ti.e);
+                    }
+                }
+                grid_dependency_wait();
+            }
             while (ok && run.next()) {
                 const Tile ti = locate(run.t, e, s_mt, s_off, n_tiles, kTileCols, kBM,
                                        p.group_m);
@@ -512,11 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* sA = smem + stage * kStageBytes;
                     uint8_t* sB = sA + kABytes;
-                    mbar_arrive_expect_tx(&full_bar[stage], p.a_rows * kBK + 2 * kBHalf);
-                    // rows of W1 and of W3, or two halves of W2's
-                    tma_load_3d(sB, &tmB0, &full_bar[stage], kb * kBK, ti.n0, ti.e);
-                    tma_load_3d(sB + kBHalf, kSwiGLU ? &tmB1 : &tmB0, &full_bar[stage], kb * kBK,
-                                kSwiGLU ? ti.n0 : ti.n0 + kAccCols / 2, ti.e);
+                    if (kSwiGLU || issued >= ahead) {
+                        mbar_arrive_expect_tx(&full_bar[stage], p.a_rows * kBK + 2 * kBHalf);
+                        // rows of W1 and of W3, or two halves of W2's
+                        tma_load_3d(sB, &tmB0, &full_bar[stage], kb * kBK, ti.n0, ti.e);
+                        tma_load_3d(sB + kBHalf, kSwiGLU ? &tmB1 : &tmB0, &full_bar[stage],
+                                    kb * kBK, kSwiGLU ? ti.n0 : ti.n0 + kAccCols / 2, ti.e);
+                    }
                     tma_load_2d(sA, &tmA, &full_bar[stage], kb * kBK, ti.row0);
                     issued_mask |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -727,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(&tmem_slot, kTmemCols);
         tmem_relinquish_pair();
     }
-    grid_dependency_wait();
+    if (kSwiGLU) grid_dependency_wait();
     tile_prefix(p.offsets, p.E, p.R, kPairRows, s_off, s_mt);
     tc_fence_before_sync();
     __syncthreads();
@@ -738,6 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int n_tiles = (p.n_out + p.tile_cols - 1) / p.tile_cols;
     const int kb_count = (p.K + kBK - 1) / kBK;
     const int tiles = s_mt[p.E] * n_tiles;
+    if (!kSwiGLU && warp != 0) grid_dependency_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -746,6 +769,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
             bool ok = true;
             const uint32_t leader_full0 = map_to_cta(smem_u32(&full_bar[0]), 0);
+            int ahead = 0;  // stages whose weights are on their way already
+            if constexpr (!kSwiGLU) {
+                if (p.stall_after < 0 && me < tiles) {
+                    const Tile ti = locate(me, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows,
+                                           p.group_m);
+                    for (; ahead < kPairStages && ahead < kb_count; ++ahead) {
+                        if (leader) mbar_arrive_expect_tx(&full_bar[ahead], 2 * kPairStageBytes);
+                        tma_load_3d_pair(smem + ahead * kPairStageBytes + kABytes, &tmB0,
+                                         leader_full0 + ahead * (uint32_t)sizeof(uint64_t),
+                                         ahead * kBK, ti.n0 + rank * 128, ti.e);
+                    }
+                }
+                grid_dependency_wait();
+            }
             for (int t = me; t < tiles && ok; t += npairs) {
                 const Tile ti = locate(t, e, s_mt, s_off, n_tiles, p.tile_cols, kPairRows,
                                        p.group_m);
@@ -763,12 +800,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint8_t* sA = smem + stage * kPairStageBytes;
                     uint8_t* sB = sA + kABytes;
                     const uint32_t bar = leader_full0 + stage * (uint32_t)sizeof(uint64_t);
-                    if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kPairStageBytes);
+                    const bool fresh = kSwiGLU || issued >= ahead;
+                    if (leader && fresh)
+                        mbar_arrive_expect_tx(&full_bar[stage], 2 * kPairStageBytes);
                     if (kSwiGLU) {
                         tma_load_3d_pair(sB, &tmB0, bar, kb * kBK, ti.n0 + rank * 64, ti.e);
                         tma_load_3d_pair(sB + kPairBBytes / 2, &tmB1, bar, kb * kBK,
                                          ti.n0 + rank * 64, ti.e);
-                    } else {
+                    } else if (fresh) {
                         tma_load_3d_pair(sB, &tmB0, bar, kb * kBK, ti.n0 + rank * 128, ti.e);
                     }
                     tma_load_2d_pair(sA, &tmA, bar, kb * kBK, arow);

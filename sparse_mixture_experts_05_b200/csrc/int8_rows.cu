@@ -149,8 +149,9 @@ template <int NU, bool kScatter, bool kWarpRow>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const uint4* __restrict__ x, int64_t rows, int units,
                     const int32_t* __restrict__ map, int k, uint4* __restrict__ xq,
-                    float* __restrict__ xs, uint32_t* zero, int64_t zero_words) {
+                    float* __restrict__ xs, uint32_t* zero, int64_t zero_words, bool early) {
     __shared__ uint32_t s_max[8];
+    if (early) launch_dependents();
     grid_dependency_wait();
     const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
     const int threads = kWarpRow ? 32 : blockDim.x;
@@ -234,9 +235,10 @@ __global__ void __launch_bounds__(kSmallThreads)
 // A warp a row up to 1536 values, when there are rows for it: less than 8 warps of a
 // block would have work, or wait for the others (32792 rows of 768: 14 us by warps, 20
 // by blocks; 4099 rows of 2048 to 8 places each: 14 and 12).
+// `early`: the next kernel may start beside this one.
 template <bool kScatter>
 int launch_quantize(const void* x, int64_t rows, int cols, const int32_t* map, int k, int8_t* xq,
-                    float* xs, uint32_t* zero, int64_t zero_words, cudaStream_t st) {
+                    float* xs, uint32_t* zero, int64_t zero_words, bool early, cudaStream_t st) {
     const int units = cols / 16;
     const bool by_warp = units <= 96 && rows >= 1024;
     const int threads = by_warp ? 256 : std::min(256, (units + 31) / 32 * 32);
@@ -251,7 +253,7 @@ int launch_quantize(const void* x, int64_t rows, int cols, const int32_t* map, i
                                       : quantize_kernel<0, kScatter, false>);
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(threads), 0, st,
                       static_cast<const uint4*>(x), rows, units, map, k,
-                      reinterpret_cast<uint4*>(xq), xs, zero, zero_words) == cudaSuccess
+                      reinterpret_cast<uint4*>(xq), xs, zero, zero_words, early) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -577,13 +579,17 @@ int launch_dispatch_quantize(const moe_shape& s, const int32_t* idx, const void*
     }
     const int rc = launch_index(s, idx, offsets, perm_tok, inv, stream);
     if (rc || s.T == 0) return rc;
-    return launch_quantize<true>(x, s.T, s.d, inv, s.k, xq, xs, zero, zero_words, stream);
+    return launch_quantize<true>(x, s.T, s.d, inv, s.k, xq, xs, zero, zero_words, false,
+                                 stream);
 }
 
 int launch_quantize_rows(const void* h, int max_rows, int cols, const int32_t* n_rows, int8_t* hq,
                          float* hs, cudaStream_t stream) {
+    // The down product loads its first weights before it waits for these rows.  Few rows: it may
+    // start beside them (whole call, 2 rows: 85.4 -> 83.6 us, 32: 250.8 -> 249.7, 2048: 61.9 -> 61.4).
+    // Many are held up by its CTAs (12306 rows of 1424: 211 -> 217 us).
     return int8rows::launch_quantize<false>(h, max_rows, cols, n_rows, 1, hq, hs, nullptr, 0,
-                                            stream);
+                                            max_rows <= 2048, stream);
 }
 
 int launch_quantize_weights(int E, int K, int N, const void* W, int8_t* Wq, float* scale,
