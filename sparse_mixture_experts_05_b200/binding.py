@@ -641,10 +641,12 @@ def _given(t, name: str, like):
 
 def _queue(stream, device: int):
     """The handle of `stream`, of the current device, or of its current stream."""
-    if stream is not None and stream.device_index != device:
+    if stream is None:
+        return _stream(None) if _raw_stream is None else _raw_stream(device)
+    if stream.device_index != device:
         raise ValueError(f"stream is of cuda:{stream.device_index}, "
                          f"the current device is cuda:{device}")
-    return _stream(stream)
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype, like, stream):

@@ -316,7 +316,8 @@ def test_expired_waits_are_reported_and_the_next_call_is_exact(T):
 # ------------------------------------------------------------------ borders
 
 @pytest.mark.parametrize("T,E,k", [(1024, 8, 1), (1025, 8, 1), (128, 32, 8), (205, 32, 5), (128, 33, 8),
-                                   (205, 33, 5), (64, 512, 16), (65, 512, 16), (2, 40, 16)])
+                                   (205, 33, 5), (64, 512, 16), (65, 512, 16), (2, 40, 16),
+                                   (70, 16, 16), (200, 32, 16)])
 def test_dispatch_where_the_kernels_change(T, E, k):
     """1024 slots and one more, 32 experts and one more, the most experts and slots."""
     x, idx = _x(T, 64, 1), _idx(T, E, k, 2)
