@@ -344,10 +344,21 @@ constexpr uint32_t kNumber = (1u << kNumberBits) - 1u;
 constexpr float kFull = 16777215.0f;   // 2^24 - 1: the value of the largest choice
 constexpr float kNone = 8388608.0f;    // 2^23
 
+// A key's number part.  A lane's places that no expert fills count on past the last expert, so
+// their numbers may need more than 9 bits (510 experts in 15 groups of two lanes: up to 524); such
+// a key holds -inf and is never selected, but its number must not reach the value part.
+__host__ __device__ constexpr uint32_t number_part(int number) {
+    return (kNumber - (uint32_t)number) & kNumber;
+}
+static_assert(number_part(0) == kNumber && number_part(kScoredMaxE - 1) == kNumber + 1 - kScoredMaxE,
+              "lower numbers make higher keys");
+static_assert(number_part(kScoredMaxE) <= kNumber && number_part(4 * kScoredMaxE) <= kNumber,
+              "numbers past the last expert stay within the number part");
+
 __device__ __forceinline__ uint32_t make_key(float c, float top, const Args& a, int number) {
-    if (a.whole_keys) return (ordered(c) & 0xffff0000u) | (kNumber - (uint32_t)number);
+    if (a.whole_keys) return (ordered(c) & 0xffff0000u) | number_part(number);
     const float v = fmaxf(fmaf(c - top, a.steps, kFull), kNone);
-    return (__float_as_uint(v) << kNumberBits) | (kNumber - (uint32_t)number);
+    return (__float_as_uint(v) << kNumberBits) | number_part(number);
 }
 // bf16 keys: -inf is below every number's key
 __device__ __forceinline__ bool selectable(uint32_t key, const Args& a) {

@@ -191,6 +191,28 @@ def test_rows_with_many_nearly_equal_choices(score, E, k, groups, levels):
             _check(l, k, sc, b)
 
 
+# all ways to cut these numbers of experts into groups: where a group's experts do not fill its
+# lanes, the places behind them count past the last expert (in 21 of these pairs past 511)
+RAGGED = [(E, G) for E in (501, 504, 505, 506, 507, 510, 511, 512) for G in range(2, 33) if E % G == 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E,G", RAGGED)
+def test_groups_that_do_not_fill_their_lanes(E, G, dtype):
+    gen = torch.Generator("cuda").manual_seed(E + G)
+    bias = 0.3 * torch.randn(E, generator=gen, device="cuda")
+    l = _logits(7, E, 31 * E + G, dtype)
+    l[4] = -9.0                          # equal choices
+    l[5, :E - 3] = -INF                  # the last group alone
+    l[6, E // G:] = -INF                 # the first
+    for score in ("softmax", "sigmoid"):
+        for top in (1, 2):
+            sc = dict(score=score, n_group=G, topk_group=(G + 1) // 2, group_top=top)
+            for k in (8, 12):
+                _check(l, k, sc)
+                _check(l, k, sc, bias)
+
+
 def test_equal_choices_go_to_the_lower_index():
     l = torch.zeros(3, 256, device="cuda")
     l[1, 100:] = 1.0
