@@ -588,7 +588,8 @@ __device__ __noinline__ int keep_group_double(const L* row, const Args& a,
 // Selects a row's k experts from those whose keys do not lie below the k-th by more
 // than `band` key values: their float64 choices, one a lane, by the whole warp.
 // `row` and `bias` lie in shared memory in the lanes' order; `kept`: bit i / group_size * group_lanes is set if the group of expert i stays.
-// Lane r < k gets the expert of slot r; false if there are more than 32.
+// Lane r < k gets the expert of slot r; false if there are more than 32, or fewer than k (the k
+// slots' own keys are among them, so this says that the keys are not what they were).
 template <typename L, int V>
 __device__ __noinline__ bool select_close(const L* row, const Args& a,
                                           const float* bias, int lane, float top,
@@ -612,7 +613,7 @@ __device__ __noinline__ bool select_close(const L* row, const Args& a,
         if (in && at < 32) list[at] = i;
         count += __popc(all);
     }
-    if (count > 32) return false;
+    if (count > 32 || count < a.k) return false;
     __syncwarp();
     const int i = lane < count ? list[lane] : 0x7fffffff;
     double v = -INFINITY;

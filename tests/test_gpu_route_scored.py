@@ -213,6 +213,24 @@ def test_groups_that_do_not_fill_their_lanes(E, G, dtype):
                 _check(l, k, sc, bias)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,k", [(510, 15, 8), (510, 30, 16), (511, 7, 8), (507, 3, 12), (504, 6, 2), (501, 3, 5)])
+@pytest.mark.parametrize("ties", [2, 20, 40])
+def test_ties_at_the_last_place_in_groups_that_do_not_fill_their_lanes(score, E, G, k, ties):
+    """`ties` equal choices, spread over the groups, around the k-th place: fewer than the slots,
+    a few more, and more than a warp decides at once."""
+    gen = torch.Generator("cuda").manual_seed(E + ties)
+    l = -2.0 - torch.rand(9, E, generator=gen, device="cuda")
+    for t in range(9):
+        at = torch.randperm(E, generator=gen, device="cuda")
+        l[t, at[:k // 2]] = 1.0 + torch.rand(k // 2, generator=gen, device="cuda")
+        l[t, at[k // 2:k // 2 + ties]] = 0.5
+    for top in (1, 2):
+        sc = dict(score=score, n_group=G, topk_group=G, group_top=top)
+        _check(l, k, sc)
+        _check(l, k, sc, torch.zeros(E, device="cuda"))
+
+
 def test_equal_choices_go_to_the_lower_index():
     l = torch.zeros(3, 256, device="cuda")
     l[1, 100:] = 1.0
