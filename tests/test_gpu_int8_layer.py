@@ -157,6 +157,36 @@ def test_sums_past_24_bits(T):
     _check_experts(shape, _idx(T, 2, 1, 1), x, (W1, W3, W2))
 
 
+@pytest.mark.parametrize("T", [400, 60000])
+def test_swiglu_is_float32_exact_far_from_zero_too(T):
+    """Every h within 10 2^-24 of SiLU(a) b, rounded once, for a down to -80: all 16 channels of a row
+    hold one h, so its 8-bit values are +-127, and a weight of 127 scaled by
+    1 / 127 brings it back as o (three float32 roundings, which bf16 does not show).  a and b
+    are exact: whole sums times powers of two.  11 2^-24 allows for this test's own
+    rounding by way of float32."""
+    xq = torch.randint(-127, 128, (T, 16), generator=_gen(1), device="cuda").to(torch.int8)
+    w1 = torch.randint(-127, 128, (16,), generator=_gen(2), device="cuda").to(torch.int8)
+    w3 = torch.randint(-127, 128, (16,), generator=_gen(3), device="cuda").to(torch.int8)
+    xs = torch.exp2(-torch.randint(9, 12, (T,), generator=_gen(4), device="cuda").float())
+    a = (xq.double() @ w1.double()) * xs.double()
+    b = (xq.double() @ w3.double()) * xs.double()
+    keep = (a > -80) & (a < 80) & (b.abs() > 1.0)
+    xq[~keep] = 0
+    one = torch.ones(1, 16, device="cuda")
+    W2 = torch.zeros(1, 16, 16, dtype=torch.int8, device="cuda")
+    W2[:, :, 3] = 127
+    weights = ((w1.expand(1, 16, 16).contiguous(), one), (w3.expand(1, 16, 16).contiguous(), one),
+               (W2, one / 127.0))
+    offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    o, ws = moe.moe_expert_swiglu_int8((T, 16, 16, 1, 1), xq, xs, offsets, *weights)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    h = torch.where(keep, a * torch.sigmoid(a) * b, 0.0)
+    ends = torch.stack([(h * (1.0 + s * 11 * 2.0 ** -24)).bfloat16() for s in (-1, 1)]).double()
+    got = o.double()
+    assert torch.all((got >= ends.amin(0)[:, None]) & (got <= ends.amax(0)[:, None]))
+    assert T < 1000 or int((keep & (a < -20)).sum()) > 5000
+
+
 @pytest.mark.parametrize("T", [24, 640])
 def test_same_bits_whatever_else_is_in_the_batch(T):
     shape = (T, 512, 768, 8, 2)
