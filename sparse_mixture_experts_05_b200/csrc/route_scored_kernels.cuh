@@ -167,7 +167,11 @@ __device__ __forceinline__ float warp_max_float(float v) { return from_key(warp_
 
 // exp(l - m) with l <= m; 1 where they are equal (both infinite among it).
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
-__device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+// Relative to e^-|l|, so that values below float32's smallest normal number (l < -87.3) do not read 0.
+__device__ __forceinline__ float sigmoid(float l) {
+    const float e = expf(-fabsf(l));
+    return __fdiv_rn(l >= 0.0f ? 1.0f : e, 1.0f + e);
+}
 __device__ __forceinline__ double sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
 
 // The row's largest logit and the sum of exp(l - m) over its live experts.
@@ -423,7 +427,7 @@ __device__ __forceinline__ void merge_best(uint32_t (&a)[KL], const uint32_t* b,
 __device__ __forceinline__ float sigmoid_ratio(float l, float M) {
     const float e = expf(-fabsf(l));
     const float top = l >= 0.0f ? 1.0f : (M < 0.0f ? exp_below(l, M) : e);
-    return __fdividef(top, 1.0f + e);
+    return __fdiv_rn(top, 1.0f + e);
 }
 
 // ------------------------------------------------------------------ forward
@@ -906,9 +910,9 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
         float total = w;  // over the slots, in pairs
         for (int off = a.slots >> 1; off > 0; off >>= 1)
             total += __shfl_xor_sync(kAll, total, off);
-        w = taken ? __fdividef(w, total) : 0.0f;
+        w = taken ? __fdiv_rn(w, total) : 0.0f;
     } else if (taken) {
-        w = a.sigmoid ? sigmoid(lv) : __fdividef(exp_below(lv, m), sum);
+        w = a.sigmoid ? sigmoid(lv) : __fdiv_rn(exp_below(lv, m), sum);
     }
     if (t < a.T && sub < a.k) {
         idx[(int64_t)t * a.k + sub] = chosen;

@@ -121,6 +121,26 @@ def test_infinite_nan_and_lowest_logits(score, renorm, grouped, biased):
         assert abs(float(gate[7].sum()) - 1.5) < 1e-5
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_sigmoids_below_the_smallest_normal_number(dtype):
+    """Gates and gradients of logits from -80 to -104, whose sigmoids reach float32's smallest
+    subnormals; sums of them in the gates are the renormalised ones' (tested above)."""
+    E, k = 40, 6
+    l = -(80.0 + 24.0 * torch.rand(30, E, generator=_gen(1), device="cuda")).to(dtype)
+    sc = dict(score="sigmoid", renorm=False)
+    idx, gate = _check(l, k, sc)
+    assert torch.all(gate[l.gather(1, idx.long()) > -100] > 0)
+    _check(l, k, sc, torch.linspace(-0.3, 0.3, E, device="cuda"))
+    dgate = torch.randn(30, k, generator=_gen(2), device="cuda")
+    got = moe.moe_route_scored_backward((30, 128, 128, E, k), l, moe.MoeScoring(**sc), idx, dgate)
+    want, bound = ref.route_backward(l, idx, dgate, sc)
+    step = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    # below the smallest normal number a value is off by its type's spacing, 2^-133 or 2^-149, in
+    # the result and a few times 2^-149 before it
+    least = 2.0 ** -133 if dtype == torch.bfloat16 else 2.0 ** -145
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= bound + np.abs(want) * step + least)
+
+
 def test_masked_rows_get_no_expert_whatever_they_hold():
     l = _logits(40, 64, 3)
     mask = torch.ones(40, dtype=torch.uint8, device="cuda")
