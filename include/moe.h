@@ -424,6 +424,8 @@ int moe_check_scoring(moe_shape s, moe_scoring r);
  * float32 choices lie too close to tell apart are decided in float64 (equal
  * groups: the lower one).  Renormalised gates are formed relative to the largest
  * selected score, so they do not underflow however negative the logits are.
+ * A row's experts and gates have the same bits whatever the other rows and however many
+ * they are.
  */
 int moe_route_scored(moe_shape s, moe_scoring r, const void* logits, int logits_type,
                      const float* bias, const uint8_t* mask, int32_t* idx, float* gate,

@@ -64,7 +64,7 @@ struct Args {
     int sigmoid, renorm;
     int n_group, group_size, topk_group, group_top;
     int group_lanes;  // forward: P, lanes of one group
-    int lane_size;    // forward: experts a lane takes of its group, at most V
+    int lane_size;    // forward: V, the experts that a lane takes of its group
     int aligned;      // forward: expert i is value i of the row's lanes (no padding inside)
     int biased;       // choices are scores plus a bias; otherwise logits order them
     int sums;         // groups are valued by a sum of two choices
@@ -333,7 +333,7 @@ __device__ __forceinline__ float fast_score(float l, const Args& a, float m, flo
 
 // Sigmoid: the exponent's rounding and ex2's two ulps move s by s (1 - s) (|l| 2^-24 +
 // 2^-22) < 0.9 2^-24, the sum and the reciprocal by 1.5 2^-24; bound 6 2^-24.  Softmax: the same
-// and the rounding of its sum of at most 32 + 5 terms a lane, relative to the row's
+// and the rounding of its sum, a tree of at most 5 + 5 additions, relative to the row's
 // largest score inv; bound 64 2^-24.
 __device__ __forceinline__ float score_error(const Args& a, float inv) {
     return a.sigmoid ? 3.5762787e-7f : 3.8146973e-6f * inv;
@@ -481,6 +481,17 @@ __device__ __forceinline__ R row_sum(R v) {
 #pragma unroll
     for (int off = 1; off < LPR; off <<= 1) v += __shfl_xor_sync(kAll, v, off);
     return v;
+}
+// term(0) + ... + term(N - 1), neighbours first: ((0 + 1) + (2 + 3)) + ...  With row_sum
+// behind it, the sum over a row's places is the same balanced tree however many lanes share the row
+// (empty places add 0, and a turned piece stays beside its neighbour), so a row's bits do
+// not depend on how many rows there are.
+template <int N, typename F>
+__device__ __forceinline__ float tree_sum(F term, int first = 0) {
+    if constexpr (N == 1)
+        return term(first);
+    else
+        return tree_sum<N / 2>(term, first) + tree_sum<N / 2>(term, first + N / 2);
 }
 template <int LPR>
 __device__ __forceinline__ float row_max(float v) {
@@ -683,15 +694,14 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
 
-    // this lane's logits, 16 bytes at a time from a place that turns with the lane, so
+    // this lane's logits, 16 bytes at a time in an order that differs from lane to lane, so
     // that the lanes' reads lie in different banks; value j is expert at(j)
     constexpr int kPer = 16 / (int)sizeof(L);  // values of a piece
     constexpr int kPieces = V / kPer > 0 ? V / kPer : 1;
     float l[V];
     const int turn = (sub * V / (kPer * 8)) & (kPieces - 1);
     auto at = [&](int j) {
-        return V <= kPer ? first + j
-                         : first + (((j / kPer + turn) & (kPieces - 1)) * kPer) + j % kPer;
+        return V <= kPer ? first + j : first + ((j / kPer) ^ turn) * kPer + j % kPer;
     };
     if constexpr (V >= kPer) {
 #pragma unroll
@@ -700,7 +710,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
                 uint4 u;
                 L v[kPer];
             } q;
-            q.u = *reinterpret_cast<const uint4*>(mine + ((c + turn) & (kPieces - 1)) * kPer);
+            q.u = *reinterpret_cast<const uint4*>(mine + (c ^ turn) * kPer);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) l[c * kPer + j] = fmaxf(to_float(q.v[j]), -INFINITY);
         }
@@ -715,10 +725,9 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
 #pragma unroll
         for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
         m = row_max<LPR>(m);
-        sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum += l[j] > -INFINITY ? fast_score(l[j], a, m, 1.0f) : 0.0f;
-        sum = row_sum<LPR>(sum);
+        sum = row_sum<LPR>(tree_sum<V>([&](int j) {
+            return l[j] > -INFINITY ? fast_score(l[j], a, m, 1.0f) : 0.0f;
+        }));
     }
     const float inv = a.sigmoid ? 1.0f : __fdividef(1.0f, sum);
 
@@ -1089,9 +1098,9 @@ inline Fit fit(const moe_shape& s, Args& a) {
                  : per <= 16 ? 16 : 32;
         if (per <= 32 || lanes == 32) break;
     }
-    // one group: lanes filled to the last; several: their experts spread evenly
-    a.lane_size = a.n_group == 1 ? values : per;
-    a.aligned = a.n_group == 1 || (per == values && a.group_size == values * a.group_lanes);
+    // lanes filled to the last: the experts' places then keep their order in the softmax's sum
+    a.lane_size = values;
+    a.aligned = a.n_group == 1 || a.group_size == values * a.group_lanes;
     return Fit{lanes, values};
 }
 

@@ -201,6 +201,17 @@ def test_same_bits_whatever_else_is_in_the_batch(T):
         assert torch.equal(y[t], one[0])
 
 
+def test_same_bits_in_batches_of_every_size_with_softmax_gates():
+    shape = (700, 256, 144, 60, 4)
+    weights = ref.random_weights(60, 256, 144, 3)
+    x, l = _x(700, 256, 1), torch.randn(700, 60, generator=_gen(2), device="cuda")
+    sc = moe.MoeScoring(renorm=False)
+    y = moe.moe_forward_int8(shape, x, l, sc, *weights)
+    for T in (1, 30, 500):
+        part = moe.moe_forward_int8((T, 256, 144, 60, 4), x[:T].clone(), l[:T].clone(), sc, *weights)
+        assert torch.equal(part, y[:T])
+
+
 # ------------------------------------------------------------------ combine
 
 @pytest.mark.parametrize("T,d,k", [(1, 16, 1), (5, 48, 2), (70, 272, 3), (300, 1024, 8), (64, 128, 16)])

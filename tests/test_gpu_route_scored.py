@@ -261,6 +261,25 @@ def test_equal_choices_go_to_the_lower_index():
         _check(l, 8, sc, torch.full((256,), 0.25, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E,k,groups", [(33, 2, 1), (60, 4, 1), (60, 4, 6), (100, 9, 10), (160, 6, 8), (256, 8, 1),
+                                        (256, 8, 8), (300, 12, 5), (500, 2, 1), (510, 8, 15), (512, 16, 16)])
+def test_a_rows_bits_do_not_depend_on_the_number_of_rows(E, k, groups, dtype):
+    """Few rows take 32 lanes each, many 8 or 16; the softmax's sum is the same tree."""
+    l = _logits(5000, E, E, dtype)
+    bias = 0.1 * torch.randn(E, generator=_gen(1), device="cuda")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            sc = dict(score=score, renorm=renorm, n_group=groups, topk_group=(groups + 1) // 2,
+                      group_top=2 if groups > 1 else 1)
+            for b in (None, bias):
+                idx, gate = _run(l, k, sc, b)
+                for T in (1, 77, 500, 900):
+                    s_idx, s_gate = _run(l[:T].clone(), k, sc, b)
+                    assert torch.equal(s_idx, idx[:T])
+                    assert torch.equal(s_gate, gate[:T]), (score, renorm, b is None, T)
+
+
 def test_rows_past_32_bit_offsets():
     E, k = 512, 4
     T = (1 << 31) // E + 77
