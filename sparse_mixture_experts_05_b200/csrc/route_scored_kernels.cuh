@@ -30,7 +30,7 @@
 //  3. all keys that may lie as high as the k-th, one a lane, in float64.
 //  4. all choices in float64 by the whole warp: where a biased softmax needs its sum in
 //     float64, or a selected choice lies beyond the keys' range (too few live experts
-//     among it).
+//     among it).  Groups and rows without a live expert are known without it.
 // So the selection is that of float64 scores.  A launch waits for its last warp, and
 // 16384 rows nearly always hold some of the second and third kind: with the fourth
 // attempt in place of the third, and for close groups, it took 3 to 8 us longer.
@@ -500,13 +500,13 @@ __device__ __forceinline__ float row_max(float v) {
     return v;
 }
 
-// Whether this lane's group stays.  b1, b2: its two best keys.  Each group's value is
-// known to lie in [lo, hi]; `full`: the order of the last kept and first dropped group is
-// not decided by that.
+// Whether this lane's group stays.  b1, b2: its two best keys; `live`: it has an expert that can be
+// chosen.  Each group's value is known to lie in [lo, hi]; `open`: these do not
+// decide whether the group stays.
 template <int LPR>
-__device__ __forceinline__ bool keep_group(uint32_t b1, uint32_t b2, const Args& a, float top,
-                                           float m, float inv, float error, int base, int group,
-                                           bool& full) {
+__device__ __forceinline__ bool keep_group(uint32_t b1, uint32_t b2, bool live, const Args& a,
+                                           float top, float m, float inv, float error, int base,
+                                           int group, bool& open) {
     // a group without a choice: below every other, a lower number first
     uint32_t lo = (uint32_t)(31 - (group & 31)), hi = lo;
     if (selectable(b1, a)) {
@@ -533,8 +533,14 @@ __device__ __forceinline__ bool keep_group(uint32_t b1, uint32_t b2, const Args&
             lo = 32u;
             hi = 0xffffffffu;
         }
-    } else if (!a.whole_keys && group < a.n_group) {  // dead, or beyond the range
-        hi = ordered(top);
+    } else if (live && group < a.n_group) {
+        // beyond the range: no choice above `far` (values up to 2^23 + 1/2 round to 0, and
+        // another 1/2 for the float that it is formed from), and one or two of them in the value
+        const float far = __fadd_ru(__fadd_ru(top, -8388606.0f * (1.0f / a.steps)), error);
+        lo = 32u;
+        hi = ordered(!a.sums    ? far
+                     : a.biased ? fmaxf(far, 2.0f * far)
+                                : 2.0f * (fast_score(far, a, m, inv) + score_error(a, inv)));
     }
     int above = 0, maybe = 0;  // groups surely, and possibly, above this one
     for (int g = 0; g < a.n_group; ++g) {
@@ -546,7 +552,7 @@ __device__ __forceinline__ bool keep_group(uint32_t b1, uint32_t b2, const Args&
         maybe += sure || (not_below && g != group);
     }
     const bool in = group < a.n_group;
-    full |= in && above < a.topk_group && maybe >= a.topk_group;
+    open = in && above < a.topk_group && maybe >= a.topk_group;
     return in && maybe < a.topk_group;
 }
 
@@ -566,14 +572,16 @@ __device__ __forceinline__ void merge_top3(uint32_t& b1, uint32_t& b2, uint32_t&
     b3 = max(min(lo, second), max(b3, o3));
 }
 
-// Whether this lane's group stays (bit 0), from the float64 values of its two best keys, and
-// whether these are surely the two best (bit 1): nothing else lies as high as the
-// second, and none is beyond the range.  `apart`: key values that may be the other way round.
+// Whether this lane's group stays (bit 0): `kept` says it unless the group is `open`; the open
+// groups share the places that the kept ones leave, by the float64 values of their two best
+// keys.  Bit 1: the group is not open, or these are surely its two best, because nothing
+// else lies as high as the second and none is beyond the range.  `apart`: key
+// values that may be the other way round.
 template <typename L, int V>
 __device__ __noinline__ int keep_group_double(const L* row, const Args& a,
                                               const float* bias, double m, uint32_t b1,
                                               uint32_t b2, uint32_t b3, uint32_t apart, int base,
-                                              int group) {
+                                              int group, bool kept, bool open) {
     double v = -INFINITY;
 #pragma unroll 1
     for (int r = 0; r < 2; ++r) {
@@ -586,18 +594,20 @@ __device__ __noinline__ int keep_group_double(const L* row, const Args& a,
         if (a.biased) c += (double)bias[at];
         v = r == 0 ? c : a.sums ? v + c : fmax(v, c);
     }
-    int rank = 0;
+    const unsigned opens = __ballot_sync(kAll, open) >> base;
+    const unsigned keeps = __ballot_sync(kAll, kept) >> base;
+    int rank = 0;  // kept groups, and open ones above this one
 #pragma unroll 1
     for (int g = 0; g < a.n_group; ++g) {
         const double o = __shfl_sync(kAll, v, base + g * a.group_lanes);
-        rank += o > v || (o == v && g < group);
+        const unsigned bit = 1u << (g * a.group_lanes);
+        rank += (keeps & bit) != 0 || ((opens & bit) != 0 && (o > v || (o == v && g < group)));
     }
     const bool sure = (a.sigmoid || !a.biased) &&
                       (a.whole_keys || (a.group_size == 1 ? selectable(b1, a)
                                                           : selectable(b2, a) &&
                                             (b2 >> kNumberBits) - (b3 >> kNumberBits) > apart));
-    return (group < a.n_group && rank < a.topk_group ? 1 : 0) |
-           (group >= a.n_group || sure ? 2 : 0);
+    return (kept || (open && rank < a.topk_group) ? 1 : 0) | (!open || sure ? 2 : 0);
 }
 
 // Selects a row's k experts from those whose keys do not lie below the k-th by more
@@ -747,11 +757,13 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
             for (int j = 0; j < V; ++j) l[j] = biased_choice(l[j], b[at(j)], a, m, inv);
         }
     }
-    float top = 0.0f;  // the row's largest choice
+    float top = 0.0f;   // the row's largest choice
+    bool live = false;  // this lane has one
     if (!a.whole_keys) {
         top = l[0];
 #pragma unroll
         for (int j = 1; j < V; ++j) top = fmaxf(top, l[j]);
+        live = top > -INFINITY;
         top = row_max<LPR>(top);
     }
     uint32_t key[V > KL ? V : KL];
@@ -790,8 +802,10 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
             const uint32_t o2 = __shfl_xor_sync(kAll, b2, off);
             merge_top2(b1, b2, o1, o2);
         }
-        kept = keep_group<LPR>(b1, b2, a, top, m, inv, key_error(8388608.0f * step), base, group,
-                               full);
+        const unsigned lives = __ballot_sync(kAll, live) >> (lane - part);  // of this group on
+        const bool group_live = (lives & (0xffffffffu >> (32 - a.group_lanes))) != 0;
+        kept = keep_group<LPR>(b1, b2, group_live, a, top, m, inv, key_error(8388608.0f * step),
+                               base, group, full);
         if (__builtin_expect(__any_sync(kAll, full && routed), 0)) {
             uint32_t b3 = best[2];
             b1 = best[0];
@@ -804,7 +818,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
                 merge_top3(b1, b2, b3, o1, o2, o3);
             }
             const int bits = keep_group_double<L, V>(row, a, s_bias, (double)m, b1, b2, b3, apart(b3),
-                                                     base, group);
+                                                     base, group, kept, full);
             const unsigned of_row = LPR == 32 ? kAll : ((1u << (LPR & 31)) - 1u) << base;
             const unsigned unsure = __ballot_sync(kAll, full) & of_row;  // by all lanes
             const unsigned exact = __ballot_sync(kAll, (bits & 2) != 0) & of_row;
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
         if (a.whole_keys) {
             // exact: equal logits go by number
         } else if (!selectable(slot, a)) {
-            full = true;  // dead, or beyond the range
+            full = top > -INFINITY;  // dead, or beyond the range
         } else {
             again = (slot >> kNumberBits) - (next >> kNumberBits) <= apart(next);
         }

@@ -141,6 +141,82 @@ def test_sigmoids_below_the_smallest_normal_number(dtype):
     assert np.all(np.abs(got.double().cpu().numpy() - want) <= bound + np.abs(want) * step + least)
 
 
+@pytest.mark.parametrize("biases", [100.0, -100.0])
+def test_groups_at_the_end_of_the_keys_range(biases):
+    """Group 0 holds the row's largest choice; the two best of group 1 and of group 2 lie 4 below
+    it, on the border of what the keys tell apart, with sums 1e-7 from each other."""
+    T, ulp = 6000, 2.0 ** -17             # the spacing of float32 between 64 and 128
+    u = (torch.rand(T, 2, generator=_gen(1), device="cuda", dtype=torch.float64) - 0.5) * 3e-7
+    half = ulp / 2                        # biased choices round up from here
+    # group 1's choices round up into the range, group 2's down out of it
+    s = torch.stack([0.5 + half + u[:, 0], 0.5 - half + u[:, 1]], 1)
+    logit = torch.log(s / (1.0 - s)).float()
+    l = torch.zeros(T, 6, device="cuda")
+    l[:, 2:4] = logit[:, :1]
+    l[:, 4:6] = logit[:, 1:]
+    bias = torch.tensor([biases, biases, biases - 4.0, biases - 4.0, biases - 4.0 + ulp, biases - 4.0 + ulp],
+                        device="cuda")
+    for top in (1, 2):
+        idx, _ = _check(l, 4, dict(score="sigmoid", n_group=3, topk_group=2, group_top=top), bias)
+        second = idx[:, 2] // 2
+        assert 1000 < int((second == 2).sum()) < 5000
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,k", [(256, 8, 8), (60, 6, 4), (96, 3, 12), (16, 16, 2), (510, 17, 6)])
+def test_groups_switched_off(E, G, k, score, dtype):
+    """Groups at -inf, at the type's lowest value, far below the others, with one live expert, and
+    rows that leave fewer live groups than stay, or none: by the logits, and by the bias."""
+    w = E // G
+    l = _logits(40, E, 77, dtype)
+    off = _logits(40, E, 77, dtype)
+    for t in range(40):
+        for g in range(G):
+            if (t * 7 + g * 5) % (2 + t % 4) == 0 or t in (30, 31):
+                off[t, g * w:(g + 1) * w] = (-INF, torch.finfo(dtype).min, -60.0, -200.0)[t % 4]
+                if t >= 20 and t != 30:
+                    off[t, g * w + t % w] = l[t, g * w + t % w]
+    by_bias = torch.zeros(E, device="cuda")
+    by_bias[:w] = -INF
+    by_bias[(G - 1) * w:] = -1e9
+    for top in (1, 2):
+        for kept in (1, (G + 1) // 2, G):
+            if k > kept * w:
+                continue
+            sc = dict(score=score, n_group=G, topk_group=kept, group_top=top)
+            _check(off, k, sc)
+            _check(off, k, sc, torch.linspace(-0.2, 0.2, E, device="cuda"))
+            _check(l, k, sc, by_bias)
+
+
+@pytest.mark.parametrize("score,top,biased", [("softmax", 1, False), ("softmax", 2, False), ("sigmoid", 1, True)])
+def test_groups_switched_off_cost_no_more_than_live_ones(score, top, biased):
+    """16384 rows of 256 experts with and without a group at -inf: about the same time (a row that goes
+    to the last attempt for its dead group made it five times as long)."""
+    E, k = 256, 8
+    sc = moe.MoeScoring(score=score, n_group=8, topk_group=4, group_top=top)
+    bias = 0.05 * torch.randn(E, generator=_gen(2), device="cuda") if biased else None
+    l = _logits(16384, E, 1)
+    off = l.clone()
+    off[:, :32] = -INF
+    idx, gate = _run(l, k, dict(score=score, n_group=8, topk_group=4, group_top=top), bias)
+
+    def time(logits):
+        best = INF
+        for _ in range(12):
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda._sleep(400000)        # the calls are queued before the first begins
+            begin.record()
+            for _ in range(8):
+                moe.moe_route_scored((16384, 128, 128, E, k), logits, sc, bias=bias, idx=idx, gate=gate)
+            end.record()
+            end.synchronize()
+            best = min(best, begin.elapsed_time(end))
+        return best
+    assert time(off) < 2.0 * time(l)
+
+
 def test_masked_rows_get_no_expert_whatever_they_hold():
     l = _logits(40, 64, 3)
     mask = torch.ones(40, dtype=torch.uint8, device="cuda")
