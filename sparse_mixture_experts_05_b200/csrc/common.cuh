@@ -61,7 +61,9 @@ __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Lets the CTAs of the stream's next kernel start once every CTA of this grid has come here.
+// Lets the CTAs of the stream's next kernel start once every CTA of this grid has come here.  That
+// kernel then runs beside this one: what this one writes it reads after its wait, and not
+// through read-only loads (__ldg).
 __device__ __forceinline__ void launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

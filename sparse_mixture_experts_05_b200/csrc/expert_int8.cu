@@ -152,7 +152,8 @@ __device__ __forceinline__ Epi make_epi(uint8_t* base, int warp, int lane) {
 }
 
 // What a warp reads of a tile from memory: four channel scales and the row scale for
-// every lane.  Loaded a tile ahead.
+// every lane.  Loaded a tile ahead.  The row scales are written by a kernel beside which the down
+// product may already run: no read-only loads of them.
 struct TileScales {
     float4 channel;
     float row;
@@ -168,7 +169,7 @@ __device__ __forceinline__ TileScales load_scales(const P& p, int e, int x0, int
     s.channel = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < p.n_out)
         s.channel = __ldg(reinterpret_cast<const float4*>(src + (int64_t)e * p.n_out + col));
-    s.row = lane < rows ? __ldg(p.row_scale + row0 + lane) : 0.0f;
+    s.row = lane < rows ? __ldcg(p.row_scale + row0 + lane) : 0.0f;
     return s;
 }
 
@@ -434,7 +435,9 @@ struct Run {
 // others epilogue.  Four stages of 48 KB; two TMEM accumulators,
 // so that a tile's epilogue overlaps the next tile's products.  The down product's weights
 // depend on nothing that the kernel before it (h's quantisation) writes, nor do the offsets:
-// its producers load the first stages' weights before they wait for that kernel.
+// its producers load the first stages' weights before they wait for that kernel.  (This needs the
+// kernel before that, the gate/up product, to have ended: it may not let its dependents start
+// early, or the offsets' and weights' writers could still be at work when the down product reads them.)
 template <bool kSwiGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,

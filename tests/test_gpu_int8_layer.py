@@ -212,6 +212,26 @@ def test_same_bits_in_batches_of_every_size_with_softmax_gates():
         assert torch.equal(part, y[:T])
 
 
+@pytest.mark.parametrize("T,d,d_ff", [(16, 512, 1024), (900, 256, 512), (1000, 128, 3600)])
+def test_calls_back_to_back_on_one_workspace(T, d, d_ff):
+    """Up to 2048 rows, so the down product starts beside the quantisation of h: two batches in
+    turn, whose row scales differ by 2^6, leave nothing of one another."""
+    shape = (T, d, d_ff, 8, 2)
+    weights = ref.random_weights(8, d, d_ff, 3)
+    rows = []
+    for s in range(2):
+        idx = _idx(T, 8, 2, s)
+        offsets, _, _, xq, xs = moe.moe_dispatch_int8(shape, idx, _x(T, d, s) * (1.0 if s else 64.0))
+        rows.append((xq, xs, offsets))
+    want = [moe.moe_expert_swiglu_int8(shape, *r, *weights)[0] for r in rows]
+    ws = moe.workspace(moe.moe_expert_swiglu_int8_workspace_bytes(shape), "cuda")
+    outs = [torch.empty_like(want[0]) for _ in range(40)]
+    for j, o in enumerate(outs):
+        moe.moe_expert_swiglu_int8(shape, *rows[j % 2], *weights, o=o, ws=ws)
+    for j, o in enumerate(outs):
+        assert torch.equal(o, want[j % 2])
+
+
 # ------------------------------------------------------------------ combine
 
 @pytest.mark.parametrize("T,d,k", [(1, 16, 1), (5, 48, 2), (70, 272, 3), (300, 1024, 8), (64, 128, 16)])
