@@ -7,10 +7,12 @@
 // by r = 127 / amax rounded up gives it: v_i and amax have 8-bit significands, so
 // a quotient that is no tie is at least 1 / (254 * 255) of its size away from one
 // (127 v_i 2 and (2n + 1) amax are integers of at most 16 bits, scaled alike),
-// against the 2^-23 by which r exceeds 127 / amax; and the only tie is
-// |v_i| = amax / 2 (127 is prime, so it has to divide 2n + 1 < 255), where the
-// quotient 63.5, exact or rounded up, goes to the even 64 either way.  The product and the
-// rounding are one fused multiply-add onto 1.5 * 2^23, whose low byte is q_i.
+// against the 2^-23 by which r exceeds 127 / amax.  A tie is 127 * 2 |v_i| = (2n + 1) amax
+// with 2n + 1 <= 253, and 127 is prime.  Either it divides 2n + 1, which is then 127: |v_i| =
+// amax / 2, and the quotient 63.5, exact or rounded up, goes to the even 64 either way.  Or it
+// divides amax's significand, which is then 254: many v_i tie, but 127 / amax is a power of two,
+// r is that very number, and the product is exact.  The product and the rounding
+// are one fused multiply-add onto 1.5 * 2^23, whose low byte is q_i.
 // Where 127 / amax would leave the float range (amax below 1e-30) both sides are
 // scaled by 2^100 first.
 #include <cuda_bf16.h>

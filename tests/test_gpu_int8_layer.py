@@ -89,6 +89,37 @@ def test_quantised_weights(E, K, N):
     assert torch.equal(torch.nan_to_num(s, nan=-1.0), torch.nan_to_num(r_s, nan=-1.0))
 
 
+def _rows_of_ties():
+    """Rows whose largest value has the significand 254 (or its half, 127): quotients by it are halves and
+    quarters of the other significands, so that every odd one ties; two rows that tie at 63.5."""
+    rows = []
+    for p in (-130, -126, -100, -7, 0, 40, 120):
+        for step in (1.0, 0.5, 0.25):
+            v = torch.arange(128, 255, dtype=torch.float64) * step     # 8-bit significands
+            v = torch.cat([v, -v, torch.tensor([254.0, -127.0])])
+            rows.append(torch.nn.functional.pad(v, (0, 272 - v.numel())) * 2.0 ** p)
+    for big in (2.0, 3.0):
+        rows.append(torch.full((272,), big / 2, dtype=torch.float64))
+        rows[-1][5], rows[-1][::2] = -big, -big / 2
+    return torch.stack(rows).float().bfloat16().cuda()
+
+
+def test_ties_between_two_8_bit_values():
+    x = _rows_of_ties()
+    T = x.shape[0]
+    q, s = ref.quantize(x)
+    f = x.double() * 127.0 / x.double().abs().amax(1, keepdim=True)
+    assert int((f - f.floor() == 0.5).sum()) > 1000        # ties there are
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    for reps in (1, 80):                                   # both of the dispatch's forms
+        xr = x.repeat(reps, 1)
+        _, _, _, xq, xs = moe.moe_dispatch_int8((T * reps, 272, 128, 1, 1), idx.repeat(reps, 1), xr)
+        assert torch.equal(xq.double(), q.repeat(reps, 1)) and torch.equal(xs, s.repeat(reps))
+    W = x[:T // 16 * 16].T.contiguous()[None]
+    wq, ws = moe.moe_quantize_weights_int8(W)
+    assert torch.equal(wq[0].double(), q[:T // 16 * 16]) and torch.equal(ws[0], s[:T // 16 * 16])
+
+
 # ------------------------------------------------------------------ products
 
 def _check_experts(shape, idx, x, weights, seed=0):

@@ -191,6 +191,19 @@ def test_quotients_round_alike_in_32_and_64_bits():
             assert np.array_equal(np.rint(prod).astype(int), want)   # the fused add rounds it once
 
 
+def test_ties_are_at_half_the_largest_value_or_have_an_exact_multiplier():
+    """127 X / (A 2^shift) half way between two whole numbers, for all bf16 significands: X is half of A's
+    value, or 127 divides A and 127 / A is a power of two."""
+    kinds = set()
+    for A in range(128, 256):
+        for shift in range(0, 9):
+            for X in range(1, 256):
+                if X <= A << shift and (2 * 127 * X) % (A << shift) == 0 and (2 * 127 * X // (A << shift)) % 2:
+                    kinds.add("half" if 2 * X == A << shift else "exact")
+                    assert 2 * X == A << shift or A == 254
+    assert kinds == {"half", "exact"}
+
+
 def test_reference_gates_by_torch():
     l = torch.randn(6, 12, generator=torch.Generator().manual_seed(1))
     for score in ("softmax", "sigmoid"):
