@@ -62,7 +62,7 @@ constexpr int blocks_per_sm(int V) { return V <= 2 ? 6 : V == 4 ? 5 : V == 8 ? 4
 struct Args {
     int T, E, k;
     int sigmoid, renorm;
-    int n_group, group_size, topk_group, group_top;
+    int n_group, group_size, topk_group;
     int group_lanes;  // forward: P, lanes of one group
     int lane_size;    // forward: V, the experts that a lane takes of its group
     int aligned;      // forward: expert i is value i of the row's lanes (no padding inside)
@@ -1083,7 +1083,6 @@ inline Args make_args(const moe_shape& s, const moe_scoring& r, bool has_bias, i
     a.n_group = r.n_group;
     a.group_size = s.E / r.n_group;
     a.topk_group = r.topk_group;
-    a.group_top = r.group_top;
     a.biased = has_bias;
     a.sums = r.n_group > 1 && r.group_top > 1;
     a.whole_keys = esize == 2 && !has_bias;
