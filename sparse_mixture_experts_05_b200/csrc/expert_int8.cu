@@ -78,7 +78,6 @@ struct Params {
     int group_m;              // m-tiles per rasterisation group
     int stall_after;
     int may_cut;              // tiles may be cut along K
-    int cut_units;            // see Run
     int a_rows;               // rows of an A box
 };
 
@@ -368,12 +367,17 @@ __device__ __forceinline__ void write_parts(const Params& p, const Epi& ep, cons
 }
 
 // The work of CTA `me` of `grid`: whole tiles me, me + grid, ..., or, where `may_cut`
-// and these would leave the busiest CTA more than `cut_units` units above the average,
-// an equal run of the units (tile, 128 values of K).  Storing and adding parts
-// costs about 7 us and 0.2 us for each routed row, a unit about 0.5 us, which is what
-// the launcher puts into cut_units.  Measured at d = 4096, d_ff = 14336, 8 experts, top-2,
-// whole / cut, us: gate/up product of 1 token 44 / 44, of 16 tokens 151 / 147, of 64
-// 153 / 165; down product of 1 token 50 / 28, of 16 79 / 86, of 64 80 / 104.
+// and that spares the busiest CTA enough, an equal run of the units (tile, 128 values of K).
+// Enough, in units of about 0.5 us: 12.5 for storing and adding parts at all, 2 for each row of a
+// tile (of the mean of them) and another fifth for each part of it, since whoever adds them
+// takes row after row and part after part, and a quarter for each row of the batch, which are all
+// stored.  Over 436 products of 1 to 500 rows, 1 to 64 experts, K 512 to 14000, the better way
+// is missed by 0.2 % of the call in the mean, by 23 % at the most (with 14 and 3/8 a
+// row of the batch alone: 4 % and fivefold).  Whole / cut, us, of the whole call:
+// down product of K = 14336, 8 experts, 2 rows 99 / 75, 8 rows 203 / 196, 32 rows 256 / 267; of K =
+// 8192, 4 experts, 2 rows 49 / 38, 8 rows 60 / 56, 64 rows 65 / 97; of K = 9184, one expert,
+// 24 rows 51 / 196; gate/up product of K = 4096, 8 experts, 32 rows 258 / 255, 64 rows 262 / 267;
+// of K = 3312, one expert, 22 rows 31 / 185.
 // Of a run, the parts of tiles at its two ends come first, so that whoever adds a
 // tile's parts has whole tiles to hide that behind.
 struct Run {
@@ -381,13 +385,18 @@ struct Run {
     int kb_count, step;
     int t, kb0, kb1;  // the current tile and its part
 
-    __device__ __forceinline__ Run(int me, int grid, int tiles, int kbs, bool may_cut,
-                                   int cut_units) {
+    __device__ __forceinline__ Run(int me, int grid, int m_tiles, int n_tiles, int kbs, bool may_cut,
+                                   int rows) {
+        const int tiles = m_tiles * n_tiles;
         kb_count = kbs;
         units = (int64_t)tiles * kbs;
         active = min((int64_t)grid, units);
         const int64_t rounds = (tiles + grid - 1) / grid;
-        if (!may_cut || (rounds * kbs - cut_units) * grid <= units) {
+        const float spared = (float)(rounds * kbs) - (float)units / (float)active;
+        const float tile_rows = (float)rows / (float)m_tiles;
+        const float parts = (float)active / (float)tiles;
+        const float enough = 12.5f + tile_rows * (2.0f + 0.2f * parts) + 0.25f * (float)rows;
+        if (!may_cut || !(spared > enough)) {  // (no tiles: NaN)
             u0 = (int64_t)me * kbs;
             u1 = units;
             skip = (int64_t)(grid - 1) * kbs;
@@ -483,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kTileCols = kSwiGLU ? kAccCols / 2 : kAccCols;  // output columns of a tile
     const int n_tiles = (p.n_out + kTileCols - 1) / kTileCols;
     const int kb_count = (p.K + kBK - 1) / kBK;
-    Run run(blockIdx.x, gridDim.x, s_mt[p.E] * n_tiles, kb_count, p.may_cut != 0,
-            p.cut_units);
+    Run run(blockIdx.x, gridDim.x, s_mt[p.E], n_tiles, kb_count, p.may_cut != 0, s_off[p.E]);
     if (!kSwiGLU && warp != 0) grid_dependency_wait();
 
     if (warp == 0) {
@@ -1019,7 +1027,6 @@ int launch_single(const moe_shape& s, const int8_t* a, const int8_t* b0, const i
     // 128 rows, 110 with 8)
     p.a_rows = (int)std::min<int64_t>(kBM, (p.R + 7) / 8 * 8);
     p.may_cut = may_cut;
-    p.cut_units = 14 + 3 * p.R / 8;
     p.part_rows = (int)std::min<int64_t>(kBM, p.R);
     p.group_m = group_of(kBM, p.K);
     CUtensorMap ma, mb0, mb1;

@@ -263,6 +263,33 @@ def test_calls_back_to_back_on_one_workspace(T, d, d_ff):
         assert torch.equal(o, want[j % 2])
 
 
+@pytest.mark.parametrize("d,d_ff,E", [(3312, 848, 1), (944, 9184, 1), (2048, 8192, 4)])
+def test_few_rows_take_no_longer_than_many(d, d_ff, E):
+    """Rows below 512 may have their tiles cut along K; where that does not pay they are not: at no
+    number of rows does the call take much longer than with 512 (it took up to five times as
+    long for 22 rows of one expert)."""
+    weights = ref.random_weights(E, d, d_ff, 3)
+
+    def time(R):
+        shape = (R, d, d_ff, E, 1)
+        offsets, _, _, xq, xs = moe.moe_dispatch_int8(shape, _idx(R, E, 1, R), _x(R, d, 1))
+        o, ws = moe.moe_expert_swiglu_int8(shape, xq, xs, offsets, *weights)
+        best = INF
+        for _ in range(12):
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda._sleep(400000)            # the calls are queued before the first begins
+            begin.record()
+            for _ in range(5):
+                moe.moe_expert_swiglu_int8(shape, xq, xs, offsets, *weights, o=o, ws=ws)
+            end.record()
+            end.synchronize()
+            best = min(best, begin.elapsed_time(end))
+        return best
+    many = time(512)
+    for R in (1, 4, 22, 64, 200):
+        assert time(R) < 1.4 * many, R
+
+
 # ------------------------------------------------------------------ combine
 
 @pytest.mark.parametrize("T,d,k", [(1, 16, 1), (5, 48, 2), (70, 272, 3), (300, 1024, 8), (64, 128, 16)])
