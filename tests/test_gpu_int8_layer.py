@@ -218,6 +218,21 @@ def test_swiglu_is_float32_exact_far_from_zero_too(T):
     assert T < 1000 or int((keep & (a < -20)).sum()) > 5000
 
 
+@pytest.mark.parametrize("T", [100, 600])
+def test_swiglu_where_the_exponential_overflows(T):
+    """a from -88 to -10000, where e^-a or the quotient leaves float32's range: h is 0 or next to it, never NaN."""
+    xq = torch.full((T, 16), 100, dtype=torch.int8, device="cuda")
+    xs = torch.linspace(88.0, 10000.0, T, device="cuda") / (16 * 100 * 100)
+    W = torch.full((1, 16, 16), 100, dtype=torch.int8, device="cuda")
+    one = torch.ones(1, 16, device="cuda")
+    offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    for up in (one, -one):
+        o, _ = moe.moe_expert_swiglu_int8((T, 16, 16, 1, 1), xq, xs, offsets, (W, -one), (W, up), (W, one))
+        assert torch.all(o.float().abs() <= 1e-20)
+    o, _ = moe.moe_expert_swiglu_int8((T, 16, 16, 1, 1), xq, xs, offsets, (W, one), (W, one), (W, one))
+    assert torch.all(torch.isfinite(o)) and torch.all(o > 0)         # SiLU(a) = a on the other side
+
+
 @pytest.mark.parametrize("T", [24, 640])
 def test_same_bits_whatever_else_is_in_the_batch(T):
     shape = (T, 512, 768, 8, 2)
