@@ -177,7 +177,8 @@ def _shape_of(T, d, d_ff, E, k) -> MoeShape:
 
 
 def _shape(shape) -> MoeShape:
-    return _shape_of(*map(int, shape))  # passed by value: one object serves a shape's calls
+    T, d, d_ff, E, k = map(int, shape)
+    return _shape_of(T, d, d_ff, E, k)  # passed by value: one object serves a shape's calls
 
 
 def _p(t):

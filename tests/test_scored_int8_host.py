@@ -247,3 +247,10 @@ def test_a_shape_is_read_anew_by_every_call():
     assert binding._shape(shape).T == 4
     T.add_(1)
     assert binding._shape(shape).T == 5
+
+
+@pytest.mark.parametrize("shape", [(4, 128, 128, 8), (4, 128, 128, 8, 2, 1), ()])
+def test_a_shape_of_another_length_is_a_value_error(shape):
+    for call in (moe.moe_check_shape, moe.moe_check_shape_int8, moe.moe_forward_workspace_bytes):
+        with pytest.raises(ValueError):
+            call(shape)
