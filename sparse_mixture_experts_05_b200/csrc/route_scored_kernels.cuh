@@ -29,8 +29,8 @@
 //     as high as the k-th.
 //  3. all keys that may lie as high as the k-th, one a lane, in float64.
 //  4. all choices in float64 by the whole warp: where a biased softmax needs its sum in
-//     float64, or a selected choice lies beyond the keys' range (too few live experts
-//     among it).  Groups and rows without a live expert are known without it.
+//     float64, or a selected choice lies beyond the keys' range.  Groups without a live
+//     expert, and slots that no live expert is left for, are known without it.
 // So the selection is that of float64 scores.  A launch waits for its last warp, and
 // 16384 rows nearly always hold some of the second and third kind: with the fourth
 // attempt in place of the third, and for close groups, it took 3 to 8 us longer.
@@ -849,19 +849,31 @@ __global__ void __launch_bounds__(kForwardWarps * 32)
             slot = best[j];
             next = j + 1 < KL ? best[j + 1 < KL ? j + 1 : j] : out;
         }
-    bool again = false;
+    bool again = false, empty = false;
     if (sub < a.k) {
         if (a.whole_keys) {
             // exact: equal logits go by number
         } else if (!selectable(slot, a)) {
-            full = top > -INFINITY;  // dead, or beyond the range
+            empty = top > -INFINITY;  // no live expert is left for it, or one beyond the range
         } else {
             again = (slot >> kNumberBits) - (next >> kNumberBits) <= apart(next);
         }
     }
     int chosen = sub < a.k && selectable(slot, a) ? number_of(slot) : -1;
 
-    if (__builtin_expect(__any_sync(kAll, (full || again) && routed), 0)) {
+    if (__builtin_expect(__any_sync(kAll, (full || again || empty) && routed), 0)) {
+        if (__any_sync(kAll, empty && routed)) {
+            bool beyond = false;  // this lane has a live expert whose key says nothing
+#pragma unroll 1
+            for (int j = 0; j < V; ++j) {
+                float c = fmaxf(to_float(mine[j]), -INFINITY);
+                if (a.biased) c = biased_choice(c, s_bias[sub * V + j], a, m, inv);
+                beyond |= kept && c > -INFINITY && !selectable(make_key(c, top, a, 0), a);
+            }
+            const unsigned of_row = LPR == 32 ? kAll : ((1u << (LPR & 31)) - 1u) << base;
+            const unsigned beyonds = __ballot_sync(kAll, beyond) & of_row;
+            full |= empty && beyonds != 0;
+        }
         unsigned fulls = __ballot_sync(kAll, full && routed), close = 0u;
         if (a.sigmoid || !a.biased) {
             // second attempt, for all rows of the warp alike

@@ -190,31 +190,67 @@ def test_groups_switched_off(E, G, k, score, dtype):
             _check(l, k, sc, by_bias)
 
 
-@pytest.mark.parametrize("score,top,biased", [("softmax", 1, False), ("softmax", 2, False), ("sigmoid", 1, True)])
+def _time_route(l, sc, bias, idx, gate):
+    T, E = l.shape
+    best = INF
+    for _ in range(12):
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda._sleep(400000)            # the calls are queued before the first begins
+        begin.record()
+        for _ in range(8):
+            moe.moe_route_scored((T, 128, 128, E, idx.shape[1]), l, sc, bias=bias, idx=idx, gate=gate)
+        end.record()
+        end.synchronize()
+        best = min(best, begin.elapsed_time(end))
+    return best
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,k", [(64, 1, 6), (256, 8, 8), (60, 6, 12), (8, 1, 2), (300, 5, 16)])
+def test_rows_with_fewer_live_experts_than_slots(E, G, k, score, dtype):
+    """0 to 9 experts above the others, which are at -inf, far below, or both."""
+    gen = _gen(E + k)
+    l = _logits(80, E, 5, dtype)
+    for t in range(80):
+        at = torch.randperm(E, generator=gen, device="cuda")
+        rest = at[min(t % 10, E):]
+        l[t, rest] = (-INF, -70.0, -90.0, -INF)[t // 20]
+        if t >= 60 and len(rest) > 3:
+            l[t, rest[:2]] = torch.tensor([-55.0, -80.0], device="cuda").to(dtype)
+    for top in (1, 2):
+        sc = dict(score=score, n_group=G, topk_group=(G + 1) // 2, group_top=top)
+        for renorm in (True, False):
+            sc["renorm"] = renorm
+            _check(l, k, sc)
+            _check(l, k, sc, torch.linspace(-0.2, 0.2, E, device="cuda"))
+            _check(l, k, sc, torch.linspace(-9.0, 9.0, E, device="cuda"))
+
+
+@pytest.mark.parametrize("score,top,biased", [("softmax", 1, False), ("softmax", 2, False), ("sigmoid", 1, True),
+                                              ("softmax", 0, False), ("sigmoid", 0, True)])
 def test_groups_switched_off_cost_no_more_than_live_ones(score, top, biased):
     """16384 rows of 256 experts with and without a group at -inf: about the same time (a row that goes
-    to the last attempt for its dead group made it five times as long)."""
+    to the last attempt for its dead group made it five times as long).  The same without
+    groups (top 0) and with fewer live experts than slots."""
     E, k = 256, 8
+    if top == 0:
+        sc = moe.MoeScoring(score=score)
+        bias = 0.05 * torch.randn(E, generator=_gen(2), device="cuda") if biased else None
+        l = _logits(16384, E, 1)
+        off = l.clone()
+        off[:, 5:] = -INF
+        idx, gate = _run(off, k, dict(score=score), bias)
+        assert torch.all(idx[:, :5] >= 0) and torch.all(idx[:, 5:] == -1)
+        assert _time_route(off, sc, bias, idx, gate) < 2.0 * _time_route(l, sc, bias, idx, gate)
+        return
     sc = moe.MoeScoring(score=score, n_group=8, topk_group=4, group_top=top)
     bias = 0.05 * torch.randn(E, generator=_gen(2), device="cuda") if biased else None
     l = _logits(16384, E, 1)
     off = l.clone()
     off[:, :32] = -INF
     idx, gate = _run(l, k, dict(score=score, n_group=8, topk_group=4, group_top=top), bias)
-
-    def time(logits):
-        best = INF
-        for _ in range(12):
-            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            torch.cuda._sleep(400000)        # the calls are queued before the first begins
-            begin.record()
-            for _ in range(8):
-                moe.moe_route_scored((16384, 128, 128, E, k), logits, sc, bias=bias, idx=idx, gate=gate)
-            end.record()
-            end.synchronize()
-            best = min(best, begin.elapsed_time(end))
-        return best
-    assert time(off) < 2.0 * time(l)
+    assert _time_route(off, sc, bias, idx, gate) < 2.0 * _time_route(l, sc, bias, idx, gate)
 
 
 def test_masked_rows_get_no_expert_whatever_they_hold():
