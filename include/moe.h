@@ -422,7 +422,9 @@ int moe_check_scoring(moe_shape s, moe_scoring r);
  * the softmax among themselves.  Slots with idx -1 get no row from the dispatch
  * and no term in the combine.  The selection is that of float64 scores: rows whose
  * float32 choices lie too close to tell apart are decided in float64 (equal
- * groups: the lower one).  Renormalised gates are formed relative to the largest
+ * groups: the lower one).  Without a bias the logits themselves order the experts, so those
+ * whose scores are equal in float64 (sigmoids of logits above 37) go by their logits, not by
+ * their ids.  Renormalised gates are formed relative to the largest
  * selected score, so they do not underflow however negative the logits are.
  * A row's experts and gates have the same bits whatever the other rows and however many
  * they are.
@@ -439,7 +441,9 @@ int moe_route_scored(moe_shape s, moe_scoring r, const void* logits, int logits_
  * outside 0..E-1, or names an expert whose logit is -inf or NaN, add nothing
  * (their dgate is not looked at); an expert named by several slots gets their
  * sum.  Only s.T, s.E, s.k, r.score, r.renorm and r.scale matter, but all of r is
- * checked.
+ * checked.  dgate is the caller's: nothing in this library forms the gradient of what comes
+ * behind the gates (moe_aux_loss depends on the logits through the scores of all experts, not
+ * through the gates).
  */
 int moe_route_scored_backward(moe_shape s, moe_scoring r, const void* logits, int logits_type,
                               const int32_t* idx, const float* dgate, void* dlogits,
@@ -478,6 +482,7 @@ int moe_dispatch_int8(moe_shape s, const int32_t* idx, const void* x, int32_t* o
  *     hq, hs = h's rows quantised,   o = (hq W2q^T) hs s2  (bf16)
  *   xq [T*k,d] int8, xs [T*k] float, offsets [E+1] int32 (from moe_dispatch_int8) (in)
  *   W1q, W3q [E,d_ff,d] int8 with s1, s3 [E,d_ff]; W2q [E,d,d_ff] int8 with s2 [E,d] (in)
+ *   (8-bit values from -127 to 127, as the quantisers give them)
  *   o [T*k,d] bf16 (out)
  *   ws: >= moe_expert_swiglu_int8_workspace_bytes(s) bytes of device memory
  * The products are summed exactly in int32 and scaled in float32, row scale first;

@@ -701,7 +701,9 @@ def moe_route_scored(shape, logits, scoring: MoeScoring, bias=None, mask=None, i
 
     `bias` [E] float32 steers the selection only; rows whose `mask` [T] uint8 is 0 get no expert.
     Returns (idx [T, k] int32, gate [T, k] float32); idx -1 (gate 0) marks a slot that
-    no expert fills.  Only T, E and k of `shape` are used."""
+    no expert fills.  Only T, E and k of `shape` are used.  Like every call here it gives plain values:
+    logits that require a gradient give gates without a graph, and moe_route_scored_backward is
+    called with their gradient."""
     T, d, d_ff, E, k = shape
     _given(logits, "logits", logits)
     dev = torch.cuda.current_device()
@@ -720,7 +722,8 @@ def moe_route_scored_backward(shape, logits, scoring: MoeScoring, idx, dgate, dl
                               stream=None):
     """Gradient of moe_route_scored's gates to the logits, in the logits' type.
 
-    `idx` is the forward call's; `dgate` [T, k] float32 the gates' gradient."""
+    `idx` is the forward call's; `dgate` [T, k] float32 the gates' gradient, which the caller forms
+    (for a training step around these calls: nothing in this package does)."""
     T, d, d_ff, E, k = shape
     _given(logits, "logits", logits)
     dev = torch.cuda.current_device()

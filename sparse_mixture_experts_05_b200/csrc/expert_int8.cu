@@ -25,10 +25,11 @@
 // comes last, and every SM reads the same share of the weights.
 //
 // What bounds them: a small batch the weights' bytes (16 tokens at d = 4096, d_ff =
-// 14336, 8 experts: 147 + 79 us for 0.94 + 0.47 GB, 6.4 and 5.9 TB/s); a large one the
-// tensor cores under the power limit (4096 tokens: 700 + 340 us, 2.75 and 2.83 Pop/s);
-// many small experts both, with rows padded to 128 (2051 tokens, 64 experts, d =
-// 2048, d_ff = 1424, top-6: 97 + 68 us).
+// 14336, 8 experts: 151 + 81 us for 0.94 + 0.47 GB, 6.2 and 5.8 TB/s); a large one the
+// tensor cores under the power limit (4096 tokens: 720 + 340 us where a launch stands alone, 2.67 and
+// 2.83 Pop/s; calls one after another take 1300 us with the 50 of h's rows in between); many
+// small experts both, with rows padded to 128 (2051 tokens, 64 experts, d = 2048, d_ff = 1424,
+// top-6: 103 + 69 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -985,12 +986,13 @@ enum Plan { kCut, kDealt, kPairs };
 // From 512 routed rows there are enough tiles, and enough rows for parts to be dear
 // (512 tokens, d = 4096, d_ff = 14336, 8 experts, top-2: 163 us whole, 278 cut).
 // Pairs read a third fewer bytes into the SMs for the same products but pad rows to
-// 256, not 128: they win at long K, where that traffic decides, and for the gate/up
-// product only once experts have many rows.  Single / pairs, us, K and rows an
-// expert: down product 768, 240: 77 / 98; 1424, 192: 68 / 68; 3584, 256: 20 / 18;
-// 8192, 256: 96 / 84; 14336, 1024: 378 / 340; 14336, 4096: 1316 / 1230; gate/up
-// product 1024, 256: 25 / 30; 2048, 192: 97 / 101; 2048, 256: 149 / 159; 4096, 128:
-// 163 / 184; 4096, 1024: 700 / 710; 4096, 4096: 2585 / 2464.
+// 256, not 128.  Down product, change of the whole call with pairs for single CTAs over 13 to 39
+// shapes each (4 to 32 experts, 128 to 2048 rows of each, d = 1024 to 4096): K = 1424 -3 %, 2048
+// 0, 2560 -1 %, 3584 -3 %, 4096 -1 %, 5120 -3 % in the mean, between -17 and +10 % (the worst
+// at every K is 8 experts of 512 rows give or take 20, 2 or 3 tiles of 256 each); K = 768 and 240 rows
+// of each of 128 experts 77 us single, 98 in pairs.  So nothing is won for sure below K = 3500.  Gate/up
+// product, K = 4096 and 5120: 1024 rows of an expert +1 to -6 %, 1280 0 to -3 %, 1536 0 to -1 %, 2048
+// -1 to -4 %, 3584 -1 to -3 %; 128 rows 163 us single, 184 in pairs; K = 2048 and 192 rows 97 and 101.
 Plan plan_of(const moe_shape& s, int K, bool swiglu) {
     const int64_t R = (int64_t)s.T * s.k;
     if (R < 512) return kCut;

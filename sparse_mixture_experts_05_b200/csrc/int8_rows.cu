@@ -588,8 +588,9 @@ int launch_dispatch_quantize(const moe_shape& s, const int32_t* idx, const void*
 int launch_quantize_rows(const void* h, int max_rows, int cols, const int32_t* n_rows, int8_t* hq,
                          float* hs, cudaStream_t stream) {
     // The down product loads its first weights before it waits for these rows.  Few rows: it may
-    // start beside them (whole call, 2 rows: 85.4 -> 83.6 us, 32: 250.8 -> 249.7, 2048: 61.9 -> 61.4).
-    // Many are held up by its CTAs (12306 rows of 1424: 211 -> 217 us).
+    // start beside them.  Change of the whole call, us, over d_ff = 768 to 5120: 8 experts, 256 to 2048
+    // rows -0.1 to -1.5; 64 experts -3.7 to +1.0 (d_ff = 1424: +0.1 to +2.8).  Many rows of many
+    // experts are held up by its CTAs: 8192 rows of 64 experts -0.9 to +4.6 (of 8: -0.2 to -2.7).
     return int8rows::launch_quantize<false>(h, max_rows, cols, n_rows, 1, hq, hs, nullptr, 0,
                                             max_rows <= 2048, stream);
 }
