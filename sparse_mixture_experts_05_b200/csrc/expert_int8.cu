@@ -251,7 +251,7 @@ __device__ __forceinline__ float2 scaled(int s0, int s1, float2 rs, float2 chann
 // ex2.approx and rcp.approx of packed pairs, 6 instructions an element, are off by another |a| 2^-24
 // and no more than 2 % faster (1024 tokens, d = 1024, d_ff = 3584, 8 experts: 61.4 and 62.5 us;
 // 2051 tokens to 64 experts 212 and 214; 4096 tokens of d = 4096 alike); the IEEE division with its
-// branch costs 5 to 40 % (87.9, 257 and 1400 us).
+// branch costs 4 to 40 % (87.9, 257 and 1400 us).
 __device__ __forceinline__ float silu_times(float a, float b) {
     return __fmul_rn(__fdividef(a, __fadd_rn(1.0f, expf(-a))), b);
 }
@@ -373,7 +373,7 @@ __device__ __forceinline__ void write_parts(const Params& p, const Epi& ep, cons
 // tile (of the mean of them) and another fifth for each part of it, since whoever adds them
 // takes row after row and part after part, and a quarter for each row of the batch, which are all
 // stored.  Over 436 products of 1 to 500 rows, 1 to 64 experts, K 512 to 14000, the better way
-// is missed by 0.2 % of the call in the mean, by 23 % at the most (with 14 and 3/8 a
+// is missed by 0.25 % of the call in the mean, by 23 % at the most (with 14 and 3/8 a
 // row of the batch alone: 4 % and fivefold).  Whole / cut, us, of the whole call:
 // down product of K = 14336, 8 experts, 2 rows 99 / 75, 8 rows 203 / 196, 32 rows 256 / 267; of K =
 // 8192, 4 experts, 2 rows 49 / 38, 8 rows 60 / 56, 64 rows 65 / 97; of K = 9184, one expert,
